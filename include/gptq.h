@@ -344,6 +344,97 @@ int gptq_silu_mul(const void* gate, const void* up, int dtype, int64_t count, vo
 /* out = a + b, elementwise over `count` values (the residual connection). */
 int gptq_add(const void* a, const void* b, int dtype, int64_t count, void* out, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Answering with a quantized layer: rotary positions per token, a paged key/value cache of
+ * 16, 8 or 4 bits, and attention of a chunk of new tokens over it.  The pages quantize a
+ * model in order to generate with it (chapter 5 §5.2) and leave this part to the model's
+ * runtime; the formulas are the usual ones, written out here.  `dtype` is GPTQ_F16 or
+ * GPTQ_BF16 throughout.  q, k and v are [tokens, heads, head_dim] with unit stride inside a
+ * head; their token and head strides are given in elements, so that the heads of one fused
+ * projection can be passed as they lie.  Strides and pointers must keep every head 16-byte
+ * aligned (strides multiples of 8 elements, pointers of 16 bytes; else UNSUPPORTED).
+ * Asynchronous; results do not depend on the run.
+ */
+
+/* Scaling rules of gptq_rotary_frequencies. */
+enum gptq_rotary_scaling {
+  GPTQ_ROTARY_NONE = 0,   /* base^(-2i/r) */
+  GPTQ_ROTARY_LINEAR = 1, /* divided by factor */
+  GPTQ_ROTARY_NTK = 2,    /* base * factor^(r/(r-2)): the slowest pair is divided by factor, the fastest kept */
+  GPTQ_ROTARY_YARN = 3    /* pairs that turn less than beta_slow times in original_len are divided by factor,
+                             those that turn more than beta_fast times kept, a linear ramp between; values are
+                             multiplied by 0.1 ln(factor) + 1 */
+};
+/* Angle per position of each of the rotary_dim/2 pairs, in double precision, written to HOST
+ * memory inv_freq[rotary_dim/2], and the factor on rotated values in *attention_factor.
+ * rotary_dim even, > 0 (> 2 for NTK); base > 1; factor >= 1; original_len > 0 and
+ * beta_fast > beta_slow > 0 for YARN. */
+int gptq_rotary_frequencies(int rotary_dim, double base, int scaling, double factor, int64_t original_len,
+                            double beta_fast, double beta_slow, double* inv_freq, float* attention_factor);
+
+/* Rotary positions of q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim] (k may be
+ * NULL with kv_heads = 0): the pairs of the first rotary_dim values of each head turn by
+ * positions[t] * inv_freq[i] and are multiplied by attention_factor; the others are copied.
+ * Pairs are (i, i + rotary_dim/2), or (2i, 2i + 1) with interleaved != 0.  Angles are taken
+ * and reduced in double precision, so far positions keep their accuracy; a negative position
+ * turns back.  positions [tokens] and inv_freq [rotary_dim/2] are device memory.  In place
+ * where q_out == q (k_out == k) with equal strides; otherwise the outputs must not overlap
+ * the inputs.  head_dim a multiple of 8, at most 512; rotary_dim even, <= head_dim. */
+int gptq_rotary(const void* q, const void* k, int dtype, int64_t tokens, int heads, int kv_heads, int head_dim,
+                int rotary_dim, int interleaved, int64_t q_token_stride, int64_t q_head_stride,
+                int64_t k_token_stride, int64_t k_head_stride, const int32_t* positions, const double* inv_freq,
+                float attention_factor, void* q_out, void* k_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                int64_t ko_token_stride, int64_t ko_head_stride, void* stream);
+
+/* A paged cache: k and v [pages, kv_heads, page_size, row], page_size 16, 32, 64, 128 or 256,
+ * head_dim 64 or 128 (else UNSUPPORTED).  bits 16: row = head_dim values of `dtype`, scales and
+ * zeros NULL.  bits 8 or 4: row = head_dim * bits / 8 bytes of codes, least significant bits
+ * first, with scales float32 and zeros uint8 [pages, kv_heads, page_size], one pair per vector:
+ *   lo = min(0, min x), hi = max(0, max x) (an all-zero vector: -1 and 1),
+ *   scale = (hi - lo) / (2^bits - 1) (both steps rounded to float32),
+ *   zero = rint(-lo / scale), code = rint(x / scale) + zero, both kept in [0, 2^bits - 1],
+ * the quotients exact before they are rounded (half to even).  The value behind a code is
+ * float32(scale * (code - zero)).  A vector with a NaN or an infinity, or a range over float32's,
+ * gets scale NaN and codes 0.
+ * Slot s is row s % page_size of page s / page_size. */
+
+/* Store token t's k and v [tokens, kv_heads, head_dim] in slot slots[t] (device, int32).  A slot
+ * outside the cache, as -1 for a padded token, is left out.  The slots of one call must differ:
+ * what a slot named twice holds is not defined. */
+int gptq_cache_write(const void* k, const void* v, int dtype, int64_t tokens, int kv_heads, int head_dim,
+                     int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                     void* k_cache, void* v_cache, float* k_scales, uint8_t* k_zeros, float* v_scales,
+                     uint8_t* v_zeros, int bits, int64_t pages, int page_size, const int32_t* slots, void* stream);
+
+/* Read the vectors of `count` slots back into k and v [count, kv_heads, head_dim] of `dtype`
+ * (contiguous), each value rounded once (bits 16: copied; `dtype` is the cache's).  A slot
+ * outside the cache reads as zeros. */
+int gptq_cache_read(const void* k_cache, const void* v_cache, const float* k_scales, const uint8_t* k_zeros,
+                    const float* v_scales, const uint8_t* v_zeros, int bits, int64_t pages, int page_size,
+                    const int32_t* slots, int64_t count, int kv_heads, int head_dim, int dtype, void* k, void* v,
+                    void* stream);
+
+/* Attention of new tokens over a paged cache that already holds their keys and values.
+ * Sequence s of `seqs` has the rows q_starts[s] .. q_starts[s+1]-1 of q [tokens, heads,
+ * head_dim] and out (contiguous, same shape), n of them, and kv_lens[s] = L keys, key j in row
+ * j % page_size of page page_table[s * table_width + j / page_size].  Its row i stands at
+ * position L - n + i and sees the keys 0 .. position (causal != 0) or 0 .. L-1; head h reads
+ * kv head h / (heads / kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j, softmax over the keys that are seen.
+ * A row that sees no key is written as zeros; rows of no sequence are left as they were.  What
+ * lies in keys that a row does not see, NaN or infinity included, does not reach it.  Values
+ * behind 8- and 4-bit codes may be rounded once to 16 bits before they are multiplied.
+ * heads a multiple of kv_heads; heads / kv_heads at most 64.  max_q_len: the most rows of a
+ * sequence (longer ones would lose rows), at most `tokens`.  q_starts [seqs + 1] runs upwards
+ * inside 0 .. tokens; a length above table_width * page_size is cut to it and a page id
+ * outside the cache is read as the nearest one inside. */
+int gptq_paged_attention(const void* q, int dtype, int64_t tokens, int heads, int kv_heads, int head_dim,
+                         int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
+                         const float* k_scales, const uint8_t* k_zeros, const float* v_scales,
+                         const uint8_t* v_zeros, int bits, int64_t pages, int page_size, const int32_t* page_table,
+                         int64_t table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t seqs,
+                         int64_t max_q_len, int causal, float scale, void* out, void* stream);
+
 /*
  * gptq_factor_hessian for callers that cannot allocate device memory.
  * The paper has no counterpart: this is a deployment variant of the factor call.

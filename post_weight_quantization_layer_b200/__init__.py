@@ -23,5 +23,13 @@ from .api import (  # noqa: F401
     quantized_linear,
     reorder_act_order,
 )
+from .kvcache import (  # noqa: F401
+    cache_read,
+    cache_write,
+    new_cache,
+    paged_attention,
+    rotary,
+    rotary_frequencies,
+)
 
 __version__ = "0.1.0"

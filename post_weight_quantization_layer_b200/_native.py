@@ -67,6 +67,19 @@ _SIGNATURES = {
     "gptq_attention": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_i64, c_int, c_int, c_int, c_void_p, c_void_p]),
     "gptq_silu_mul": (c_int, [c_void_p, c_void_p, c_int, c_i64, c_void_p, c_void_p]),
     "gptq_add": (c_int, [c_void_p, c_void_p, c_int, c_i64, c_void_p, c_void_p]),
+    "gptq_rotary_frequencies": (c_int, [c_int, ctypes.c_double, c_int, ctypes.c_double, c_i64, ctypes.c_double,
+                                        ctypes.c_double, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_float)]),
+    "gptq_rotary": (c_int, [c_void_p, c_void_p, c_int, c_i64, c_int, c_int, c_int, c_int, c_int, c_i64, c_i64, c_i64,
+                            c_i64, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_i64,
+                            c_void_p]),
+    "gptq_cache_write": (c_int, [c_void_p, c_void_p, c_int, c_i64, c_int, c_int, c_i64, c_i64, c_i64, c_i64, c_void_p,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_i64, c_int, c_void_p,
+                                 c_void_p]),
+    "gptq_cache_read": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_i64, c_int,
+                                c_void_p, c_i64, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
+    "gptq_paged_attention": (c_int, [c_void_p, c_int, c_i64, c_int, c_int, c_int, c_i64, c_i64, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_i64, c_int, c_void_p, c_i64,
+                                     c_void_p, c_void_p, c_i64, c_i64, c_int, c_float, c_void_p, c_void_p]),
     "gptq_device_status": (c_int, [c_void_p, c_int]),
     "gptq_trim_workspace": (c_int, []),
     "gptq_status_string": (ctypes.c_char_p, [c_int]),

@@ -1,0 +1,177 @@
+"""Refusals of the serving operators (C ABI and Python binding) and the rotary frequencies (host
+code), without a GPU.  Only calls that are rejected, or that have no work, reach the library:
+pointers are fake and never read."""
+
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_layer_b200 as gq
+from oracle import serving_ref as R
+from post_weight_quantization_layer_b200 import _native
+from post_weight_quantization_layer_b200.build import build
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+FAKE, ODD = 0x10000, 0x10004
+
+
+@pytest.fixture(scope="module")
+def L():
+    build()
+    return _native.lib()
+
+
+def _rotary(L, **kw):
+    a = dict(q=FAKE, k=FAKE, dtype=2, tokens=4, heads=8, kv_heads=2, d=128, r=128, inter=0, qt=1024, qh=128, kt=256, kh=128,
+             pos=FAKE, freq=FAKE, factor=1.0, qo=2 * FAKE, ko=2 * FAKE, qot=1024, qoh=128, kot=256, koh=128, stream=None)
+    a.update(kw)
+    return L.gptq_rotary(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(pos=None), INVALID), (dict(freq=None), INVALID),
+    (dict(qo=None), INVALID), (dict(ko=None), INVALID), (dict(dtype=0), INVALID), (dict(dtype=9), INVALID),
+    (dict(tokens=-1), INVALID), (dict(heads=0), INVALID), (dict(kv_heads=-1), INVALID), (dict(r=0), INVALID),
+    (dict(r=7), INVALID), (dict(r=130), INVALID), (dict(d=0), INVALID), (dict(d=132, r=4), UNSUPPORTED),
+    (dict(d=520, r=4), UNSUPPORTED), (dict(qt=1028), UNSUPPORTED), (dict(kh=4), UNSUPPORTED), (dict(q=ODD), UNSUPPORTED),
+    (dict(ko=ODD), UNSUPPORTED), (dict(qoh=2), UNSUPPORTED), (dict(qo=FAKE, qot=2048), INVALID),
+    (dict(ko=FAKE, koh=256), INVALID), (dict(tokens=0), OK), (dict(tokens=0, q=None, qo=None, k=None, ko=None, pos=None), OK)])
+def test_rotary_rejections(L, kw, status):
+    assert _rotary(L, **kw) == status
+
+
+def _write(L, **kw):
+    a = dict(k=FAKE, v=FAKE, dtype=2, tokens=4, heads=2, d=128, kt=256, kh=128, vt=256, vh=128, kc=FAKE, vc=FAKE, ks=FAKE,
+             kz=FAKE, vs=FAKE, vz=FAKE, bits=8, pages=4, page=64, slots=FAKE, stream=None)
+    a.update(kw)
+    return L.gptq_cache_write(*a.values())
+
+
+CACHE = [(dict(kc=None), INVALID), (dict(vc=None), INVALID), (dict(ks=None), INVALID), (dict(vz=None), INVALID),
+         (dict(bits=2), INVALID), (dict(bits=3), INVALID), (dict(bits=0), INVALID), (dict(pages=0), INVALID),
+         (dict(page=0), INVALID), (dict(page=8), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(page=512), UNSUPPORTED),
+         (dict(pages=1 << 26), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(d=0), INVALID),
+         (dict(dtype=0), INVALID), (dict(heads=0), INVALID), (dict(kc=ODD), UNSUPPORTED), (dict(vs=ODD), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("kw,status", CACHE + [
+    (dict(k=None), INVALID), (dict(slots=None), INVALID), (dict(tokens=-1), INVALID), (dict(kt=100), UNSUPPORTED),
+    (dict(vh=4), UNSUPPORTED), (dict(v=ODD), UNSUPPORTED), (dict(tokens=0), OK),
+    (dict(tokens=0, bits=16, ks=None, kz=None, vs=None, vz=None), OK), (dict(tokens=0, k=None, v=None, slots=None), OK)])
+def test_cache_write_rejections(L, kw, status):
+    assert _write(L, **kw) == status
+
+
+def _read(L, **kw):
+    a = dict(kc=FAKE, vc=FAKE, ks=FAKE, kz=FAKE, vs=FAKE, vz=FAKE, bits=8, pages=4, page=64, slots=FAKE, count=3, heads=2,
+             d=128, dtype=1, k=FAKE, v=FAKE, stream=None)
+    a.update(kw)
+    return L.gptq_cache_read(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", CACHE + [(dict(k=None), INVALID), (dict(count=-1), INVALID), (dict(v=ODD), UNSUPPORTED),
+                                               (dict(slots=None), INVALID), (dict(count=0), OK)])
+def test_cache_read_rejections(L, kw, status):
+    assert _read(L, **kw) == status
+
+
+def _attend(L, **kw):
+    a = dict(q=FAKE, dtype=2, tokens=4, q_heads=8, heads=2, d=128, qt=1024, qh=128, kc=FAKE, vc=FAKE, ks=FAKE, kz=FAKE,
+             vs=FAKE, vz=FAKE, bits=8, pages=4, page=64, table=FAKE, width=4, lens=FAKE, starts=FAKE, seqs=2, max_q=4,
+             causal=1, scale=0.1, out=FAKE, stream=None)
+    a.update(kw)
+    return L.gptq_paged_attention(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", CACHE + [
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
+    (dict(starts=None), INVALID), (dict(tokens=-1), INVALID), (dict(seqs=-1), INVALID), (dict(q_heads=0), INVALID),
+    (dict(q_heads=9), INVALID), (dict(width=0), INVALID), (dict(max_q=-1), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
+    (dict(q_heads=130), UNSUPPORTED), (dict(qt=1025), UNSUPPORTED), (dict(q=ODD), UNSUPPORTED), (dict(out=ODD), UNSUPPORTED),
+    (dict(seqs=1 << 21), UNSUPPORTED), (dict(tokens=0), OK), (dict(seqs=0, table=None, lens=None), OK), (dict(max_q=0), OK)])
+def test_attention_rejections(L, kw, status):
+    assert _attend(L, **kw) == status
+
+
+@pytest.mark.parametrize("r", [64, 128, 20, 6])
+@pytest.mark.parametrize("scaling,factor,original", [(None, 1.0, 0), ("linear", 4.0, 0), ("ntk", 8.0, 0), ("yarn", 32.0, 4096),
+                                                     ("yarn", 1.0, 128)])
+def test_rotary_frequencies(L, r, scaling, factor, original):
+    f, a = gq.rotary_frequencies(r, 10000.0, scaling, factor, original, device="cpu")
+    ref, ra = R.rotary_frequencies(r, 10000.0, scaling, factor, original)
+    assert f.dtype == torch.float64 and np.allclose(f.numpy(), ref, rtol=1e-14) and abs(a - ra) <= 2.0 ** -24 * ra
+    if scaling == "ntk":  # the slowest pair is slowed by the factor, the fastest kept
+        plain, _ = R.rotary_frequencies(r)
+        assert f[0] == 1.0 and abs(f[-1] * factor / plain[-1] - 1) < 1e-12
+
+
+@pytest.mark.parametrize("kw", [dict(base=1.0), dict(base=math.inf), dict(scaling="linear", factor=0.5),
+                                dict(scaling="linear", factor=math.nan), dict(scaling="yarn", factor=2.0),
+                                dict(scaling="yarn", factor=2.0, original_len=64, beta_fast=1.0, beta_slow=1.0),
+                                dict(scaling="other")])
+def test_rotary_frequencies_rejections(L, kw):
+    with pytest.raises((ValueError, gq.GPTQError)):
+        gq.rotary_frequencies(64, device="cpu", **kw)
+    with pytest.raises(ValueError):
+        gq.rotary_frequencies(7, device="cpu")
+    with pytest.raises(gq.GPTQError):
+        gq.rotary_frequencies(2, scaling="ntk", factor=2.0, device="cpu")
+
+
+def test_oracle_quantizer_keeps_the_nearest_code():
+    """Against a search over all codes, and the scale's ends."""
+    rng = np.random.default_rng(0)
+    for bits in (4, 8):
+        x = rng.normal(size=(40, 64)) * np.exp(rng.normal(size=(40, 1)) * 3)
+        x = x.astype(np.float16).astype(np.float64)
+        c, s, z = R.quantize_vectors(x, bits)
+        every = s[:, None, None].astype(np.float64) * (np.arange(2 ** bits)[None, None] - z[:, None, None].astype(np.float64))
+        best = np.abs(x[..., None] - every).min(-1)
+        got = np.abs(x - s[:, None].astype(np.float64) * (c.astype(np.float64) - z[:, None]))
+        assert np.all(got <= best + 1e-12 * np.abs(x))
+        assert np.array_equal(R.unpack_vector_codes(R.pack_vector_codes(c, bits), bits), c)
+
+
+# ------------------------------------------------------------------ the binding's own checks
+BF = torch.bfloat16
+
+
+def _cpu_cache(bits=8, D=64, P=16):
+    return gq.new_cache(3, 2, D, P, bits, BF, device="cpu")
+
+
+def test_binding_rejections(L):
+    x = torch.zeros(5, 4, 64, dtype=BF)
+    kv = torch.zeros(5, 2, 64, dtype=BF)
+    i5 = torch.zeros(5, dtype=torch.int32)
+    f = torch.zeros(32, dtype=torch.float64)
+    table, lens, starts = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    bad = [
+        lambda: gq.rotary(x[0], None, i5, f), lambda: gq.rotary(x.float(), None, i5, f),
+        lambda: gq.rotary(x, kv.half(), i5, f), lambda: gq.rotary(x, kv[:3], i5, f), lambda: gq.rotary(x, kv[..., :32], i5, f),
+        lambda: gq.rotary(x, kv, i5.long(), f), lambda: gq.rotary(x, kv, i5[:4], f), lambda: gq.rotary(x, kv, i5, f.float()),
+        lambda: gq.rotary(x.transpose(1, 2), None, i5, f), lambda: gq.rotary(x, kv, i5, f),  # CPU tensors
+        lambda: gq.cache_write(kv, kv.half(), _cpu_cache(), i5, 8), lambda: gq.cache_write(kv, kv[:4], _cpu_cache(), i5, 8),
+        lambda: gq.cache_write(kv, kv, _cpu_cache(), i5.long(), 8), lambda: gq.cache_write(kv, kv, _cpu_cache(), i5, 5),
+        lambda: gq.cache_write(kv, kv, _cpu_cache(16), i5, 8), lambda: gq.cache_write(kv, kv, _cpu_cache(8), i5, 16),
+        lambda: gq.cache_write(kv, kv, _cpu_cache(8), i5, 4), lambda: gq.cache_write(x, x, _cpu_cache(), i5, 8),
+        lambda: gq.cache_write(kv, kv, {"k": kv}, i5, 8), lambda: gq.cache_write(kv, kv, None, i5, 8),
+        lambda: gq.cache_write(kv.half(), kv.half(), _cpu_cache(16), i5, 16),
+        lambda: gq.cache_write(kv, kv, dict(_cpu_cache(), v_zeros=i5), i5, 8),
+        lambda: gq.cache_read(_cpu_cache(), i5.float(), 8), lambda: gq.cache_read(_cpu_cache(), i5, 8, torch.float32),
+        lambda: gq.cache_read(_cpu_cache(16), i5, 16, torch.float16), lambda: gq.cache_read(_cpu_cache(), i5, 8),
+        lambda: gq.paged_attention(torch.zeros(5, 3, 64, dtype=BF), _cpu_cache(), table, lens, starts, 8),
+        lambda: gq.paged_attention(x, _cpu_cache(), table[0], lens, starts, 8),
+        lambda: gq.paged_attention(x, _cpu_cache(), table, lens, lens, 8),
+        lambda: gq.paged_attention(x, _cpu_cache(), table.long(), lens, starts, 8),
+        lambda: gq.paged_attention(x, _cpu_cache(D=128), table, lens, starts, 8),
+        lambda: gq.new_cache(1, 1, 64, bits=3, device="cpu"), lambda: gq.new_cache(1, 1, 64, dtype=torch.float32, device="cpu"),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was accepted")
