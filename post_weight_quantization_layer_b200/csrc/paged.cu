@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const Args a) {
   }
   const Seq q = sequence(a, lo);
   const int i = t - q.start;
-  if (i < 0 || i >= q.n) return;
+  if (i < 0 || i >= q.n || q.n * a.group <= kStepRows) return;
   float m, l, acc[D / 32];
   row_attention<T, D, BITS>(a, lo, h / a.group, static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs, 0, seen(a, q, i),
                             m, l, acc);
@@ -92,6 +92,8 @@ extern "C" int gptq_paged_attention(const void* q, int dtype, int64_t tokens, in
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  GPTQ_TRY(paged::run_step(a, dtype, head_dim, bits, s));
+  if (static_cast<int64_t>(a.max_q) * a.group <= paged::kStepRows) return GPTQ_OK;
   if (dtype == GPTQ_BF16)
     return head_dim == 128 ? paged::launch<__nv_bfloat16, 128>(a, bits, s) : paged::launch<__nv_bfloat16, 64>(a, bits, s);
   return head_dim == 128 ? paged::launch<__half, 128>(a, bits, s) : paged::launch<__half, 64>(a, bits, s);

@@ -139,5 +139,9 @@ __device__ __forceinline__ __half to16<__half>(float v) { return __float2half_rn
 template <>
 __device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).
+constexpr int kStepRows = 16;
+int run_step(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s);
+
 }  // namespace paged
 }  // namespace gptq
