@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 namespace gptq {
 
@@ -283,7 +284,8 @@ int gptq_device_status(void* stream, int clear) {
   const int h = hessian_device_status(static_cast<cudaStream_t>(stream), clear);
   const int g = gemm_device_status(clear);
   const int i = i8_device_status(clear);
-  return h != GPTQ_OK ? h : (g != GPTQ_OK ? g : i);
+  const int c = paged::chunk_device_status(clear);
+  return h != GPTQ_OK ? h : (g != GPTQ_OK ? g : (i != GPTQ_OK ? i : c));
 }
 
 int gptq_factor_hessian(const float* H, int64_t n_in, float damp_percent, int desc_act, double* U, int32_t* perm,

@@ -1,49 +1,8 @@
-// Attention of new tokens over a paged cache: o = sum_j softmax_j(scale q . k_j) v_j.
+// Attention of new tokens over a paged cache: o = sum_j softmax_j(scale q . k_j) v_j.  Arguments are
+// checked here; sequences with at most kStepRows rows (tokens x heads of a kv head) go to the kernel
+// of paged_step.cu, the others to that of paged_chunk.cu, each sequence by its own number of rows on
+// the device.
 #include "paged.cuh"
-
-namespace gptq {
-namespace paged {
-namespace {
-
-// One warp per (row, head): the formula as it stands, one pass with the running maximum and sum.
-template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(128) rows_kernel(const Args a) {
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int t = static_cast<int>(w / a.heads), h = static_cast<int>(w % a.heads);
-  if (t >= a.tokens) return;
-  int lo = 0, hi = a.seqs;  // the last sequence that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    (__ldg(a.starts + mid) <= t ? lo : hi) = mid;
-  }
-  const Seq q = sequence(a, lo);
-  const int i = t - q.start;
-  if (i < 0 || i >= q.n || q.n * a.group <= kStepRows) return;
-  float m, l, acc[D / 32];
-  row_attention<T, D, BITS>(a, lo, h / a.group, static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs, 0, seen(a, q, i),
-                            m, l, acc);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* o = static_cast<T*>(a.out) + (static_cast<int64_t>(t) * a.heads + h) * D;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) o[lane + 32 * c] = to16<T>(acc[c] * inv);
-}
-
-template <typename T, int D>
-int launch(const Args& a, int bits, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.tokens) * a.heads + 3) / 4);
-  if (bits == 16)
-    rows_kernel<T, D, 16><<<grid, 128, 0, s>>>(a);
-  else if (bits == 8)
-    rows_kernel<T, D, 8><<<grid, 128, 0, s>>>(a);
-  else
-    rows_kernel<T, D, 4><<<grid, 128, 0, s>>>(a);
-  return after_launch();
-}
-
-}  // namespace
-}  // namespace paged
-}  // namespace gptq
 
 using namespace gptq;
 
@@ -61,7 +20,7 @@ extern "C" int gptq_paged_attention(const void* q, int dtype, int64_t tokens, in
                        head_dim, dtype));
   if (heads % kv_heads || !(scale > 0.f && scale < INFINITY)) return GPTQ_ERR_INVALID_ARG;
   if (heads / kv_heads > 64 || heads > 65535 || seqs > (1 << 20) || table_width > (int64_t(1) << 27) ||
-      tokens * heads > (int64_t(1) << 31))
+      tokens * heads > (int64_t(1) << 30))
     return GPTQ_ERR_UNSUPPORTED;
   if (((q_token_stride | q_head_stride) & 7) || !aligned16(q) || !aligned16(out)) return GPTQ_ERR_UNSUPPORTED;
   if (!work) return GPTQ_OK;
@@ -94,7 +53,5 @@ extern "C" int gptq_paged_attention(const void* q, int dtype, int64_t tokens, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GPTQ_TRY(paged::run_step(a, dtype, head_dim, bits, s));
   if (static_cast<int64_t>(a.max_q) * a.group <= paged::kStepRows) return GPTQ_OK;
-  if (dtype == GPTQ_BF16)
-    return head_dim == 128 ? paged::launch<__nv_bfloat16, 128>(a, bits, s) : paged::launch<__nv_bfloat16, 64>(a, bits, s);
-  return head_dim == 128 ? paged::launch<__half, 128>(a, bits, s) : paged::launch<__half, 64>(a, bits, s);
+  return paged::run_chunk(a, dtype, head_dim, bits, s);
 }

@@ -142,6 +142,9 @@ __device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float v) { return _
 // paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).
 constexpr int kStepRows = 16;
 int run_step(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s);
+// paged_chunk.cu: the sequences with more rows.
+int run_chunk(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s);
+int chunk_device_status(int clear);
 
 }  // namespace paged
 }  // namespace gptq

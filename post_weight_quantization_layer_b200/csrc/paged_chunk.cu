@@ -1,0 +1,858 @@
+// Attention over a paged cache for sequences with many rows (chunks of a prompt), on the tcgen05
+// tensor cores.
+//
+// A tile is 256 rows of one kv head (row i * group + g of a sequence, so that all query heads of the kv
+// head share its keys), two halves of 128 rows with a warpgroup each.  Per 128 keys and half: scores
+// S = Q K^T into tensor memory, softmax by one thread per row, probabilities back into tensor memory
+// over the scores, O += P V from there.  While one half's softmax runs, the tensor core works on the
+// other half.  512 columns of tensor memory: two S (128 each, P over them), two O (head_dim each).
+//
+//  * Roles: warps 0-3 and 4-7 softmax, rescaling and output of their half; warp 8 issues the matrix
+//    products; warp 9 brings keys and values; warps 12-15 (8- and 4-bit caches only) turn codes into
+//    16-bit operands.  Registers move from the last two to the first.
+//  * 16-bit pages come by TMA straight into the swizzled operand tiles.  Pages of codes come by bulk
+//    copies (codes, scales and zeros of a page and head are contiguous) into a staging ring, from
+//    which the converters write operand tiles, each value rounded once to 16 bits (as cache_read
+//    gives it).
+//  * The running maximum moves only when it grows by more than 8 (base 2): until then probabilities
+//    reach 2^8 at most, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
+//  * The (row tile, 128 keys) units of the batch are cut into equal shares, one per SM, as in the
+//    kernel for few rows; cut tiles are joined by a second launch in a fixed order.
+// Bound by the exponentials and the tensor core together: 128 x 128 scores take 512 cycles of the
+// tensor core twice and 1024 cycles of the 16-per-cycle exponential unit.
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged.cuh"
+#include "paged_plan.cuh"
+#include "sm100.cuh"
+
+namespace gptq {
+namespace paged {
+namespace {
+
+using namespace sm100;
+
+constexpr int CH_ROWS = 256;  // rows of a tile
+constexpr int CH_KEYS = 128;  // keys of a unit
+constexpr uint32_t CH_WAIT = 1u << 22;
+constexpr float CH_GROW = 8.f;
+
+__device__ int g_chunk_status = 0;
+
+template <int D, int BITS>
+struct Cfg {
+  static constexpr int THREADS = BITS == 16 ? 384 : 512;
+  static constexpr int TILE = CH_KEYS * D * 2;         // bytes of an operand tile
+  static constexpr int NST = D == 128 ? 4 : 6;         // operand tiles in the ring
+  static constexpr int ROW = D * BITS / 8;
+  static constexpr int RAW = BITS == 16 ? 0 : ((CH_KEYS * (ROW + 5) + 127) / 128) * 128;  // codes, scales, zeros
+  static constexpr int NRAW = BITS == 16 ? 1 : (BITS == 8 ? 2 : 3);
+  static constexpr int QOFF = 0;
+  static constexpr int RING = 2 * TILE;
+  static constexpr int ROFF = RING + NST * TILE;
+  static constexpr int BARS = ROFF + NRAW * RAW;
+  static constexpr int SMEM = BARS + 512 + 1024;
+};
+
+// ------------------------------------------------------------------ the line of units
+struct Tile {
+  int kend;   // keys that the tile's last row sees
+  int units;  // of CH_KEYS keys; 1 where there is none
+};
+
+__device__ __forceinline__ Tile tile_of(const Args& a, const Seq& q, int tile) {
+  Tile t;
+  const int last = min(q.n - 1, static_cast<int>((static_cast<int64_t>(tile + 1) * CH_ROWS - 1) / a.group));
+  t.kend = seen(a, q, last);
+  t.units = max(1, (t.kend + CH_KEYS - 1) / CH_KEYS);
+  return t;
+}
+
+__device__ __forceinline__ int tiles_of(const Args& a, const Seq& q) {
+  const int64_t rows = static_cast<int64_t>(q.n) * a.group;
+  return rows > kStepRows ? static_cast<int>((rows + CH_ROWS - 1) / CH_ROWS) : 0;
+}
+
+__device__ int64_t head_units(const Args& a, int s) {  // units of one kv head of sequence s
+  const Seq q = sequence(a, s);
+  const int n = tiles_of(a, q);
+  int64_t u = 0;
+  for (int i = 0; i < n; ++i) u += tile_of(a, q, i).units;
+  return u;
+}
+
+struct Piece {
+  int64_t at, end;
+  int s, head, tile, u0, u1, units, tiles, kend;
+  Seq q;
+};
+
+__device__ __forceinline__ void enter_tile(const Args& a, Piece& p, int u0) {
+  const Tile t = tile_of(a, p.q, p.tile);
+  p.kend = t.kend;
+  p.units = t.units;
+  p.u0 = u0;
+  p.u1 = static_cast<int>(min(static_cast<int64_t>(t.units), u0 + (p.end - p.at)));
+}
+
+// The piece at position `start` of the line for a CTA whose share ends at `end`.  All threads.
+template <int THREADS>
+__device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& p, int64_t& per, int64_t* shared) {
+  int64_t all = 0, total;
+  for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += head_units(a, x);
+  block_scan<THREADS>(all, total);
+  total *= a.kv_heads;
+  per = share_of(sh, total);
+  p.at = cta * per;
+  p.end = min(total, p.at + per);
+  if (p.at >= p.end) return false;
+  int64_t base = 0;
+  for (int x0 = 0; x0 < a.seqs; x0 += THREADS) {
+    const int x = x0 + threadIdx.x;
+    const int64_t u = x < a.seqs ? head_units(a, x) * a.kv_heads : 0;
+    int64_t sum;
+    const int64_t incl = block_scan<THREADS>(u, sum);
+    const int64_t lo = base + incl - u;
+    if (u && lo <= p.at && p.at < lo + u) {
+      shared[0] = x;
+      shared[1] = p.at - lo;
+      shared[2] = u / a.kv_heads;
+    }
+    base += sum;
+    if (base > p.at) break;
+  }
+  __syncthreads();
+  p.s = static_cast<int>(shared[0]);
+  p.q = sequence(a, p.s);
+  p.tiles = tiles_of(a, p.q);
+  p.head = static_cast<int>(shared[1] / shared[2]);
+  int64_t rem = shared[1] % shared[2];
+  p.tile = 0;
+  for (;;) {
+    const int u = tile_of(a, p.q, p.tile).units;
+    if (rem < u) break;
+    rem -= u;
+    ++p.tile;
+  }
+  enter_tile(a, p, static_cast<int>(rem));
+  return true;
+}
+
+__device__ __forceinline__ void chunk_next(const Args& a, Piece& p) {
+  p.at += p.u1 - p.u0;
+  if (p.at >= p.end) return;
+  if (++p.tile == p.tiles) {
+    p.tile = 0;
+    if (++p.head == a.kv_heads) {
+      p.head = 0;
+      do {
+        ++p.s;
+        p.q = sequence(a, p.s);
+        p.tiles = tiles_of(a, p.q);
+      } while (p.tiles == 0);
+    }
+  }
+  enter_tile(a, p, 0);
+}
+
+// ------------------------------------------------------------------ instructions
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Untiled copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Byte offset of 16-byte chunk c (8 elements) of row r in an operand tile: 64-element blocks of [128 rows]
+// [128 bytes], 128-byte swizzle.
+__device__ __forceinline__ uint32_t chunk_off(int r, int c) {
+  return static_cast<uint32_t>((c >> 3) * (CH_KEYS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+struct Bars {
+  uint64_t *full, *empty, *rfull, *rempty, *qfull, *sfull, *pfull, *odone, *zero, *done;
+};
+
+// A place in a ring of N: index and phase.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == N) {
+      i = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+template <typename T, int D, int BITS>
+__global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Args a,
+                 const Share sh, float* __restrict__ part, int* __restrict__ odd) {
+  using C = Cfg<D, BITS>;
+  constexpr int SIZE = (D + 2) * CH_ROWS;  // floats of a piece left behind
+  constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0u : 1u;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int64_t plan[3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Piece p;
+  int64_t per;
+  __shared__ int any_odd;
+  if (threadIdx.x == 0) any_odd = 0;
+  if (!chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, plan)) {
+    if (threadIdx.x == 0) odd[blockIdx.x] = 0;
+    return;
+  }
+  const int64_t first = p.at;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
+  Bars b;
+  b.full = bars;
+  b.empty = b.full + C::NST;
+  b.rfull = b.empty + C::NST;
+  b.rempty = b.rfull + C::NRAW;
+  b.qfull = b.rempty + C::NRAW;
+  b.sfull = b.qfull + 2;
+  b.pfull = b.sfull + 2;
+  b.odone = b.pfull + 2;
+  b.zero = b.odone + 2;
+  b.done = b.zero + 1;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(b.done + 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&b.full[i], BITS == 16 ? 1 : 4);
+      mbar_init(&b.empty[i], 1);
+    }
+    for (int i = 0; i < C::NRAW; ++i) {
+      mbar_init(&b.rfull[i], 1);
+      mbar_init(&b.rempty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.qfull[i], 4);
+      mbar_init(&b.sfull[i], 1);
+      mbar_init(&b.pfull[i], 4);
+      mbar_init(&b.odone[i], 1);
+    }
+    mbar_init(b.zero, 1);
+    mbar_init(b.done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  bool ok = true;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax, one thread per row
+    regs_more<BITS == 16 ? 216 : 200>();
+    const int w = warp >> 2, wr = (warp & 3) * 32 + lane;  // half, row of the half
+    uint8_t* qs = smem + C::QOFF + w * C::TILE;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t S = tmem + lanes + w * 128, O = tmem + lanes + 256 + w * D;
+    uint32_t sph = 0, oph = 0;
+    for (; p.at < p.end && ok; chunk_next(a, p)) {
+      const int rows = p.q.n * a.group;
+      const int row = p.tile * CH_ROWS + w * 128 + wr;
+      if (p.tile * CH_ROWS + w * 128 >= rows) continue;  // the tile has no second half
+      const bool in = row < rows;
+      const int i = in ? row / a.group : 0, h = p.head * a.group + (in ? row - i * a.group : 0);
+      const int k0 = p.u0 * CH_KEYS, k1 = min(p.u1 * CH_KEYS, p.kend);
+      const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+      const int see = in ? min(k1, seen(a, p.q, i)) : k1;  // rows past the last: whatever comes out is not used
+      int least = see;
+      for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+      {  // this row of Q
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (p.q.start + i) * a.q_ts + h * a.q_hs);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(qs + chunk_off(wr, c)) = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.qfull[w]);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < tiles; ++j) {
+        if (!mbar_wait(&b.sfull[w], sph, CH_WAIT)) {
+          ok = false;
+          break;
+        }
+        sph ^= 1u;
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(S + c * 32, s[c]);
+        const int key = k0 + j * CH_KEYS;
+        if (key + CH_KEYS > least) {  // some row of the warp does not see all of these keys
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c][e] = key + c * 32 + e < see ? s[c][e] : -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = s[c][0];
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], s[c][e]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, (top - m) * a.scale_log2 > CH_GROW)) {
+          // all earlier products are complete: they precede these scores on the tensor core
+          const float now = fmaxf(m, top);
+          const float f = now == -INFINITY ? 1.f : ex2((m - now) * a.scale_log2);
+          m = now;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(O + c * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * f);
+            tmem_st_x32(O + c * 32, r);
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m * a.scale_log2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = ex2(fmaf(s[2 * c + (e >> 4)][(2 * e) & 31], a.scale_log2, -ref));
+            const float y = ex2(fmaf(s[2 * c + (e >> 4)][(2 * e + 1) & 31], a.scale_log2, -ref));
+            sum += x + y;
+            r[e] = pack2<T>(x, y);
+          }
+          l += sum;
+          tmem_st_x32(S + c * 32, r);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.pfull[w]);
+      }
+      if (!ok) break;
+      if (tiles) {
+        if (!mbar_wait(&b.odone[w], oph, CH_WAIT)) {
+          ok = false;
+          break;
+        }
+        oph ^= 1u;
+        tc_fence_after();
+      }
+      const bool whole = p.u0 == 0 && p.u1 == p.units;
+      float* mine =
+          whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.at == first ? 0 : 1)) * static_cast<int64_t>(SIZE);
+      const int r = w * 128 + wr;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(p.q.start) + i) * a.heads + h) * D;
+      bool fine = true;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        if (tiles) {
+          tmem_ld_32x32b_x32(O + c * 32, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) fine = fine && fabsf(o[e]) < INFINITY;
+        if (mine) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mine[(c * 32 + e) * CH_ROWS + r] = o[e];
+        } else if (in) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 v;
+            v.x = pack2<T>(o[8 * e] * inv, o[8 * e + 1] * inv);
+            v.y = pack2<T>(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+            v.z = pack2<T>(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+            v.w = pack2<T>(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+            reinterpret_cast<uint4*>(dst)[c * 4 + e] = v;
+          }
+        }
+      }
+      if (mine) {
+        mine[D * CH_ROWS + r] = m == -INFINITY ? m : m * a.scale_log2;
+        mine[(D + 1) * CH_ROWS + r] = l;
+      }
+      tc_fence_before();
+      if (in && !fine) any_odd = 1;
+    }
+  } else if (warp < 12) {
+    regs_fewer<BITS == 16 ? 72 : 40>();
+    if (warp == 8) {
+      // -------------------------------------------------------------- issue of the matrix products
+      if (lane == 0) {
+        constexpr uint32_t iqk = instr_desc(FMT, false, false, 128, CH_KEYS);
+        constexpr uint32_t ipv = instr_desc(FMT, false, true, 128, D);
+        Ring<C::NST> ring;
+        uint32_t qph = 0, pph = 0;  // phases, a bit per half
+        const uint32_t q0 = smem_u32(smem + C::QOFF), r0 = smem_u32(smem + C::RING);
+        auto qk = [&](int w, int st) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = static_cast<uint32_t>((k >> 2) * (CH_KEYS * 128) + (k & 3) * 32);
+            umma_f16(tmem + w * 128, smem_desc_sw128(q0 + w * C::TILE + off, 16, 1024),
+                     smem_desc_sw128(r0 + st * C::TILE + off, 16, 1024), iqk, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&b.sfull[w]);
+        };
+        for (; p.at < p.end && ok; chunk_next(a, p)) {
+          const int rows = p.q.n * a.group;
+          const int nw = rows > p.tile * CH_ROWS + 128 ? 2 : 1;
+          const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+          for (int w = 0; w < nw; ++w) {  // Q of this piece is in place, O of the last one is read
+            ok = ok && mbar_wait(&b.qfull[w], (qph >> w) & 1u, CH_WAIT);
+            qph ^= 1u << w;
+          }
+          if (!ok) break;
+          if (!tiles) continue;
+          if (!mbar_wait(&b.full[ring.i], ring.ph, CH_WAIT)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int w = 0; w < nw; ++w) qk(w, ring.i);
+          umma_commit(&b.empty[ring.i]);
+          ring.step();
+          for (int j = 0; j < tiles && ok; ++j) {
+            const int vst = ring.i;
+            const uint32_t vph = ring.ph;
+            ring.step();
+            const int kst = ring.i;
+            const uint32_t kph = ring.ph;
+            const bool more = j + 1 < tiles;
+            if (more) ring.step();
+            for (int w = 0; w < nw; ++w) {
+              ok = ok && mbar_wait(&b.pfull[w], (pph >> w) & 1u, CH_WAIT);
+              pph ^= 1u << w;
+              if (w == 0) ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < CH_KEYS / 16; ++k)
+                umma_f16_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8,
+                            smem_desc_sw128(r0 + vst * C::TILE + k * 2048, CH_KEYS * 128, 1024), ipv,
+                            (j > 0 || k > 0) ? 1u : 0u);
+              if (w == nw - 1) umma_commit(&b.empty[vst]);
+              if (more) {
+                if (w == 0) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
+                if (!ok) break;
+                tc_fence_after();
+                qk(w, kst);
+                if (w == nw - 1) umma_commit(&b.empty[kst]);
+              } else {
+                umma_commit(&b.odone[w]);
+              }
+            }
+          }
+        }
+        umma_commit(b.done);
+        mbar_wait(b.done, 0, CH_WAIT);
+      }
+    } else if (warp == 9) {
+      // -------------------------------------------------------------- keys and values, page by page
+      Ring<C::NST> ring;
+      Ring<C::NRAW> raw;
+      uint32_t zph = 0;
+      int issued = 0;
+      const int box = min(1 << a.page_shift, CH_KEYS), boxes = CH_KEYS / box;
+      for (; p.at < p.end && ok; chunk_next(a, p)) {
+        const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int key = (p.u0 + j) * CH_KEYS;
+          const int mykey = key + lane * box;
+          const int n = min(boxes, (p.kend - key + box - 1) / box);  // boxes that hold keys
+          const int64_t at = lane < n ? key_at(a, p.s, p.head, mykey) : 0;
+          for (int kv = 0; kv < 2; ++kv) {
+            if constexpr (BITS == 16) {
+              if (!mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
+                ok = false;
+                break;
+              }
+              uint8_t* dst = smem + C::RING + ring.i * C::TILE;
+              // the last values of a sequence: what lies behind them in the tile must be finite
+              const int rest = p.kend - key;
+              const bool tail = kv == 1 && rest < CH_KEYS;
+              uint64_t* bar = tail ? b.zero : &b.full[ring.i];
+              if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * box * D * 2));
+              __syncwarp();
+              if (lane < n) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_2d(dst + c * (CH_KEYS * 128) + lane * box * 128, kv ? &tv : &tk, bar, c * 64, static_cast<int>(at));
+              }
+              if (tail) {
+                if (!mbar_wait(b.zero, zph, CH_WAIT)) {
+                  ok = false;
+                  break;
+                }
+                zph ^= 1u;
+                for (int e = lane; e < (CH_KEYS - rest) * (D / 8); e += 32) {
+                  const int r = rest + e / (D / 8), c = e % (D / 8);
+                  *reinterpret_cast<uint4*>(dst + chunk_off(r, c)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.full[ring.i]);
+              }
+              ++issued;
+              ring.step();
+            } else {
+              if (!mbar_wait(&b.rempty[raw.i], raw.ph ^ 1u, CH_WAIT)) {
+                ok = false;
+                break;
+              }
+              uint8_t* dst = smem + C::ROFF + raw.i * C::RAW;
+              if (lane == 0) mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(n * box * (C::ROW + 5)));
+              __syncwarp();
+              if (lane < n) {
+                const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.vc : a.kc) + at * C::ROW;
+                bulk_load(dst + lane * box * C::ROW, codes, box * C::ROW, &b.rfull[raw.i]);
+                bulk_load(dst + CH_KEYS * C::ROW + lane * box * 4, (kv ? a.vs : a.ks) + at, box * 4, &b.rfull[raw.i]);
+                bulk_load(dst + CH_KEYS * (C::ROW + 4) + lane * box, (kv ? a.vz : a.kz) + at, box, &b.rfull[raw.i]);
+              }
+              ++issued;
+              raw.step();
+            }
+          }
+        }
+      }
+      // no copy of ours may still be landing in shared memory when the CTA leaves
+      if (!ok) {
+        constexpr int N = BITS == 16 ? C::NST : C::NRAW;
+        int at = BITS == 16 ? ring.i : raw.i;
+        uint32_t ph = BITS == 16 ? ring.ph : raw.ph;
+        for (int k = 0; k < min(issued, N); ++k) {
+          if (--at < 0) {
+            at += N;
+            ph ^= 1u;
+          }
+          mbar_wait(BITS == 16 ? &b.full[at] : &b.rfull[at], ph, CH_WAIT);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- codes -> 16-bit operand tiles
+    if constexpr (BITS < 16) {
+      regs_fewer<72>();
+      constexpr int PPR = D / 16;  // 16-code pieces of a row
+      const int tid = threadIdx.x - 384;
+      const int col = tid % PPR, r0 = tid / PPR;
+      Ring<C::NST> ring;
+      Ring<C::NRAW> raw;
+      for (; p.at < p.end && ok; chunk_next(a, p)) {
+        const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+        for (int jj = 0; jj < 2 * tiles; ++jj) {
+          const int rest = p.kend - (p.u0 + (jj >> 1)) * CH_KEYS;
+          if (!mbar_wait(&b.rfull[raw.i], raw.ph, CH_WAIT) || !mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
+            ok = false;
+            break;
+          }
+          const uint8_t* src = smem + C::ROFF + raw.i * C::RAW;
+          uint8_t* dst = smem + C::RING + ring.i * C::TILE;
+#pragma unroll
+          for (int x = 0; x < CH_KEYS * PPR / 128; ++x) {
+            const int r = r0 + x * (128 / PPR);
+            uint32_t out[8];
+            if (r < rest) {
+              const float s = *reinterpret_cast<const float*>(src + CH_KEYS * C::ROW + r * 4);
+              const float z = 8388608.f + static_cast<float>(src[CH_KEYS * (C::ROW + 4) + r]);
+              uint32_t wd[4];
+              if constexpr (BITS == 8) {
+                *reinterpret_cast<uint4*>(wd) = *reinterpret_cast<const uint4*>(src + r * C::ROW + col * 16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t v = wd[e >> 1];
+                  const float f0 = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650u + (e & 1) * 2)) - z;
+                  const float f1 = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651u + (e & 1) * 2)) - z;
+                  out[e] = pack2<T>(s * f0, s * f1);
+                }
+              } else {
+                *reinterpret_cast<uint2*>(wd) = *reinterpret_cast<const uint2*>(src + r * C::ROW + col * 8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t v = wd[e >> 2] >> ((e & 3) * 8);
+                  const float f0 = __uint_as_float((v & 15u) | 0x4B000000u) - z;
+                  const float f1 = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u) - z;
+                  out[e] = pack2<T>(s * f0, s * f1);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) out[e] = 0;
+            }
+            // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
+            const int o = col & 4 ? 1 : 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int hf = y ^ o;
+              *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + hf)) =
+                  hf ? make_uint4(out[4], out[5], out[6], out[7]) : make_uint4(out[0], out[1], out[2], out[3]);
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&b.full[ring.i]);
+            mbar_arrive(&b.rempty[raw.i]);
+          }
+          ring.step();
+          raw.step();
+        }
+      }
+    }
+  }
+  if (!ok) atomicExch(&g_chunk_status, kStatusTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) odd[blockIdx.x] = any_odd;
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of every tile that was cut: CTA c takes the tile that the border between shares c and
+// c + 1 cuts, unless an earlier border cuts it too.
+constexpr int CJ_THREADS = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(CJ_THREADS) chunk_join_kernel(const Args a, const Share sh, const float* __restrict__ part) {
+  __shared__ int64_t plan[3];
+  Piece p;
+  int64_t per;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) + 1;
+  const bool any = chunk_first<CJ_THREADS>(a, sh, c, p, per, plan);
+  if (!any || p.u0 == 0) return;
+  const int64_t start = p.at - p.u0, end = start + p.units;
+  if ((c - 1) * per > start) return;
+  const int64_t c0 = c - 1, c1 = (end - 1) / per;
+  constexpr int64_t SIZE = (D + 2) * CH_ROWS;
+  const int rows = min(CH_ROWS, p.q.n * a.group - p.tile * CH_ROWS);
+  for (int e = threadIdx.x; e < (D / 8) * CH_ROWS; e += CJ_THREADS) {
+    const int r = e % CH_ROWS, col = (e / CH_ROWS) * 8;
+    if (r >= rows) continue;
+    float m = -INFINITY, l = 0.f, v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int64_t x = c0; x <= c1; ++x) {
+      const float* q = part + (2 * x + (x == c0 && start != c0 * per ? 1 : 0)) * SIZE;
+      const float pm = q[D * CH_ROWS + r], pl = q[(D + 1) * CH_ROWS + r];
+      const float mm = fmaxf(m, pm), ref = mm == -INFINITY ? 0.f : mm;
+      const float f0 = ex2(m - ref), f1 = ex2(pm - ref);
+      m = mm;
+      l = l * f0 + pl * f1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * f0 + q[(col + i) * CH_ROWS + r] * f1;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = p.tile * CH_ROWS + r, i = row / a.group;
+    T* dst = static_cast<T*>(a.out) +
+             ((static_cast<int64_t>(p.q.start) + i) * a.heads + p.head * a.group + (row - i * a.group)) * D + col;
+    uint4 w;
+    w.x = pack2<T>(v[0] * inv, v[1] * inv);
+    w.y = pack2<T>(v[2] * inv, v[3] * inv);
+    w.z = pack2<T>(v[4] * inv, v[5] * inv);
+    w.w = pack2<T>(v[6] * inv, v[7] * inv);
+    *reinterpret_cast<uint4*>(dst) = w;
+  }
+}
+
+// Where a CTA met an accumulator that is not finite, rows are looked at again: a value that a row does not
+// see, NaN or infinite, has met its zero weight in the products.  One warp per (row, head) whose result
+// is not finite works it out key by key over the keys it sees.  Otherwise the launch reads the CTAs'
+// words and ends.
+template <typename T, int D, int BITS>
+__global__ void __launch_bounds__(128) chunk_redo_kernel(const Args a, const int* __restrict__ odd, int n) {
+  const int lane = threadIdx.x & 31;
+  int any = 0;
+  for (int x = threadIdx.x; x < n; x += 128) any |= __ldg(odd + x);
+  if (!__syncthreads_or(any)) return;
+  const int64_t all = static_cast<int64_t>(a.tokens) * a.heads;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); w < all; w += gridDim.x * 4) {
+    const int t = static_cast<int>(w / a.heads), h = static_cast<int>(w % a.heads);
+    int lo = 0, hi = a.seqs;  // the last sequence that starts at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      (__ldg(a.starts + mid) <= t ? lo : hi) = mid;
+    }
+    const Seq q = sequence(a, lo);
+    const int i = t - q.start;
+    if (i < 0 || i >= q.n || static_cast<int64_t>(q.n) * a.group <= kStepRows) continue;
+    T* o = static_cast<T*>(a.out) + w * D;
+    bool fine = true;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) fine = fine && fabsf(to_f32(o[lane + 32 * c])) < INFINITY;
+    if (__all_sync(0xffffffffu, fine)) continue;
+    float m, l, acc[D / 32];
+    row_attention<T, D, BITS>(a, lo, h / a.group, static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs, 0, seen(a, q, i), m,
+                              l, acc);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[lane + 32 * c] = to16<T>(acc[c] * inv);
+  }
+}
+
+// ------------------------------------------------------------------ host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// The vectors of a 16-bit cache as rows; a box is 64 elements of the keys of a page (at most 128).
+template <typename T>
+int cache_map(CUtensorMap* m, const void* base, const Args& a, int d) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return GPTQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d),
+                              (static_cast<cuuint64_t>(a.pages) * a.kv_heads) << a.page_shift};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(std::min(1 << a.page_shift, CH_KEYS))};
+  const cuuint32_t es[2] = {1, 1};
+  const CUresult r = enc(m, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GPTQ_OK : GPTQ_ERR_CUDA;
+}
+
+template <typename T, int D, int BITS>
+int run(const Args& a, cudaStream_t s) {
+  using C = Cfg<D, BITS>;
+  GPTQ_TRY(ensure_smem_limit(reinterpret_cast<const void*>(chunk_kernel<T, D, BITS>), C::SMEM));
+  CUtensorMap tk = {}, tv = {};
+  if (BITS == 16) {
+    GPTQ_TRY(cache_map<T>(&tk, a.kc, a, D));
+    GPTQ_TRY(cache_map<T>(&tv, a.vc, a, D));
+  }
+  Share sh;
+  sh.whole = 0;
+  sh.min_per = 8;
+  sh.rows_lo = kStepRows + 1;
+  sh.rows_hi = 0x7fffffff;
+  sh.grid = num_sms();
+  void* part = nullptr;
+  const size_t pieces = static_cast<size_t>(sh.grid) * 2 * (D + 2) * CH_ROWS * sizeof(float);
+  GPTQ_TRY(pool_alloc(&part, pieces + sh.grid * sizeof(int), s));
+  int* odd = reinterpret_cast<int*>(static_cast<char*>(part) + pieces);
+  chunk_kernel<T, D, BITS><<<sh.grid, C::THREADS, C::SMEM, s>>>(tk, tv, a, sh, static_cast<float*>(part), odd);
+  int st = after_launch();
+  if (st == GPTQ_OK && sh.grid > 1) {
+    chunk_join_kernel<T, D><<<sh.grid - 1, CJ_THREADS, 0, s>>>(a, sh, static_cast<const float*>(part));
+    st = after_launch();
+  }
+  if (st == GPTQ_OK) {
+    chunk_redo_kernel<T, D, BITS><<<sh.grid, 128, 0, s>>>(a, odd, sh.grid);
+    st = after_launch();
+  }
+  pool_free(part, s);
+  return st;
+}
+
+}  // namespace
+
+int run_chunk(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s) {
+#define GPTQ_CHUNK(T, D) return bits == 16 ? run<T, D, 16>(a, s) : bits == 8 ? run<T, D, 8>(a, s) : run<T, D, 4>(a, s)
+  if (dtype == GPTQ_BF16) {
+    if (head_dim == 128) GPTQ_CHUNK(__nv_bfloat16, 128);
+    GPTQ_CHUNK(__nv_bfloat16, 64);
+  }
+  if (head_dim == 128) GPTQ_CHUNK(__half, 128);
+  GPTQ_CHUNK(__half, 64);
+#undef GPTQ_CHUNK
+}
+
+int chunk_device_status(int clear) {
+  int h = 0;
+  if (cudaMemcpyFromSymbol(&h, g_chunk_status, sizeof(int)) != cudaSuccess) return GPTQ_ERR_CUDA;
+  if (clear && h != GPTQ_OK) {
+    const int z = 0;
+    cudaMemcpyToSymbol(g_chunk_status, &z, sizeof(int));
+  }
+  return h;
+}
+
+}  // namespace paged
+}  // namespace gptq
