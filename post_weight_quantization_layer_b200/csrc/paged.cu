@@ -51,7 +51,9 @@ extern "C" int gptq_paged_attention(const void* q, int dtype, int64_t tokens, in
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  GPTQ_TRY(paged::run_step(a, dtype, head_dim, bits, s));
-  if (static_cast<int64_t>(a.max_q) * a.group <= paged::kStepRows) return GPTQ_OK;
-  return paged::run_chunk(a, dtype, head_dim, bits, s);
+  const bool chunks = static_cast<int64_t>(a.max_q) * a.group > paged::kStepRows;
+  if (chunks) GPTQ_TRY(paged::run_chunk(a, dtype, head_dim, bits, s));
+  // sequences with few rows may be among long ones; there are none where a single row is more
+  if (a.group > paged::kStepRows) return GPTQ_OK;
+  return paged::run_step(a, dtype, head_dim, bits, chunks, s);
 }

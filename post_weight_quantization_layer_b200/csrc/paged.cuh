@@ -139,9 +139,35 @@ __device__ __forceinline__ __half to16<__half>(float v) { return __float2half_rn
 template <>
 __device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// The launches of one call overlap: each may start, and work out its share, while the one before it
+// drains, and waits for it before it reads what it wrote, or else before it ends, so that the end of the
+// last launch is the end of all.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_next(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return GPTQ_ERR_CUDA;
+  }
+  return after_launch();
+}
+
 // paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).
 constexpr int kStepRows = 16;
-int run_step(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s);
+// `next`: follows a launch of the same call.
+int run_step(const Args& a, int dtype, int head_dim, int bits, bool next, cudaStream_t s);
 // paged_chunk.cu: the sequences with more rows.
 int run_chunk(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s);
 int chunk_device_status(int clear);

@@ -37,6 +37,7 @@ using namespace sm100;
 
 constexpr int CH_ROWS = 256;  // rows of a tile
 constexpr int CH_KEYS = 128;  // keys of a unit
+constexpr int CH_RAW = 64;    // keys of a staging slot
 constexpr uint32_t CH_WAIT = 1u << 22;
 constexpr float CH_GROW = 8.f;
 
@@ -48,13 +49,16 @@ struct Cfg {
   static constexpr int TILE = CH_KEYS * D * 2;         // bytes of an operand tile
   static constexpr int NST = D == 128 ? 4 : 6;         // operand tiles in the ring
   static constexpr int ROW = D * BITS / 8;
-  static constexpr int RAW = BITS == 16 ? 0 : ((CH_KEYS * (ROW + 5) + 127) / 128) * 128;  // codes, scales, zeros
-  static constexpr int NRAW = BITS == 16 ? 1 : (BITS == 8 ? 2 : 3);
+  // staging of codes, scales and zeros, half a tile of keys each
+  static constexpr int RAW = BITS == 16 ? 0 : ((CH_RAW * (ROW + 5) + 127) / 128) * 128;
+  static constexpr int NRAW = BITS == 16 ? 1 : (BITS == 8 ? 4 : 6);
   static constexpr int QOFF = 0;
   static constexpr int RING = 2 * TILE;
   static constexpr int ROFF = RING + NST * TILE;
   static constexpr int BARS = ROFF + NRAW * RAW;
-  static constexpr int SMEM = BARS + 512 + 1024;
+  static constexpr int SMEM = BARS + 320 + 1024;
+  static_assert((2 * NST + 2 * NRAW + 10) * 8 + 4 <= 320, "barriers");
+  static_assert(SMEM + 160 <= 232448, "shared memory of a CTA");
 };
 
 // ------------------------------------------------------------------ the line of units
@@ -159,26 +163,69 @@ __device__ __forceinline__ void chunk_next(const Args& a, Piece& p) {
 }
 
 // ------------------------------------------------------------------ instructions
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
-__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Shared-memory descriptors as their low word (start address and leading offset, 16-byte units: a step
+// inside a tile is an addition) with a constant high word (stride 1024 bytes, version 1, 128-byte swizzle).
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+// D[tmem] (+)= A[smem] * B[smem], kind::f16.
+__device__ __forceinline__ void umma_ss(uint32_t tmem_d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16.
+__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(blo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+// Loads without their wait: the registers may be used after tmem_ld_wait() and settled().
+__device__ __forceinline__ void tmem_ld_x32_nowait(uint32_t taddr, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Orders uses of the registers after the wait that precedes it.
+__device__ __forceinline__ void settled(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                      "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -202,6 +249,34 @@ __device__ __forceinline__ void regs_fewer() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Packed fp32 pairs (the f32x2 arithmetic of sm_100).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -220,6 +295,12 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Byte offset of 16-byte chunk c (8 elements) of row r in an operand tile: 64-element blocks of [128 rows]
@@ -259,6 +340,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   Piece p;
   int64_t per;
   __shared__ int any_odd;
+  next_may_start();
   if (threadIdx.x == 0) any_odd = 0;
   if (!chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, plan)) {
     if (threadIdx.x == 0) odd[blockIdx.x] = 0;
@@ -316,26 +398,55 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t S = tmem + lanes + w * 128, O = tmem + lanes + 256 + w * D;
     uint32_t sph = 0, oph = 0;
-    for (; p.at < p.end && ok; chunk_next(a, p)) {
-      const int rows = p.q.n * a.group;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+    // a row of the tile, counted from the first token that the tile touches, is token r / group of it
+    const uint32_t recip = 65536u / a.group + 1u;  // r < 320: (r * recip) >> 16 is exact
+    auto absent = [&]() { return p.tile * CH_ROWS + w * 128 >= p.q.n * a.group; };  // the tile has no such half
+    auto skip = [&]() {
+      while (p.at < p.end && absent()) chunk_next(a, p);
+      return p.at < p.end;
+    };
+    // Q of this half of the piece p, 16 bytes a lane along the rows; rows past the last are zeros
+    auto load_q = [&]() {
+      const int row0 = p.tile * CH_ROWS, i0 = row0 / a.group, over = row0 - i0 * a.group;
+      const int rows = p.q.n * a.group - row0 - w * 128;
+      const T* base = static_cast<const T*>(a.q) + (p.q.start + i0) * a.q_ts + p.head * a.group * a.q_hs;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) {
+        const int e = x * 128 + (threadIdx.x & 127), r = e / (D / 8), c = e % (D / 8);
+        const int rr = over + w * 128 + r, i = static_cast<int>((rr * recip) >> 16);
+        const T* src = base + (r < rows ? i * a.q_ts + (rr - i * a.group) * a.q_hs + c * 8 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(qs + chunk_off(r, c))), "l"(src),
+                     "r"(r < rows ? 16 : 0)
+                     : "memory");
+      }
+    };
+    auto q_ready = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.qfull[w]);
+    };
+    bool more = skip();
+    if (more) {
+      load_q();
+      q_ready();
+    }
+    while (more) {
       const int row = p.tile * CH_ROWS + w * 128 + wr;
-      if (p.tile * CH_ROWS + w * 128 >= rows) continue;  // the tile has no second half
-      const bool in = row < rows;
+      const bool in = row < p.q.n * a.group;
       const int i = in ? row / a.group : 0, h = p.head * a.group + (in ? row - i * a.group : 0);
       const int k0 = p.u0 * CH_KEYS, k1 = min(p.u1 * CH_KEYS, p.kend);
       const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
       const int see = in ? min(k1, seen(a, p.q, i)) : k1;  // rows past the last: whatever comes out is not used
       int least = see;
       for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-      {  // this row of Q
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (p.q.start + i) * a.q_ts + h * a.q_hs);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(qs + chunk_off(wr, c)) = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.qfull[w]);
-      }
+      const bool whole = p.u0 == 0 && p.u1 == p.units;
+      float* mine =
+          whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.at == first ? 0 : 1)) * static_cast<int64_t>(SIZE);
+      T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(p.q.start) + i) * a.heads + h) * D;
+      chunk_next(a, p);
+      more = skip();
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < tiles; ++j) {
         if (!mbar_wait(&b.sfull[w], sph, CH_WAIT)) {
@@ -344,9 +455,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         sph ^= 1u;
         tc_fence_after();
+        if (j + 1 == tiles && more) load_q();  // the last scores are there: Q's place is free for the next piece's
         float s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(S + c * 32, s[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld_x32_nowait(S + c * 32, s[c]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) settled(s[c]);
         const int key = k0 + j * CH_KEYS;
         if (key + CH_KEYS > least) {  // some row of the warp does not see all of these keys
 #pragma unroll
@@ -354,14 +469,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[c][e] = key + c * 32 + e < see ? s[c][e] : -INFINITY;
         }
-        float mx[4];
+        float mx[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = s[c][0];
+        for (int c = 0; c < 8; ++c) mx[c] = fmaxf(s[0][c], s[0][c + 8]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], s[c][e]);
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int x = 16; x < 128; x += 16)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mx[c] = max3(mx[c], s[x >> 5][(x & 31) + c], s[x >> 5][(x & 31) + c + 8]);
+        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
         if (j == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, (top - m) * a.scale_log2 > CH_GROW)) {
@@ -371,36 +486,41 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           m = now;
           l *= f;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(O + c * 32, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld_x16(O + c * 16, r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * f);
-            tmem_st_x32(O + c * 32, r);
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            tmem_st_x16(O + c * 16, r);
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m * a.scale_log2;
+        const float ref = m == -INFINITY ? 0.f : -m * a.scale_log2;
+        const float2 ref2 = make_float2(ref, ref), sc2 = make_float2(a.scale_log2, a.scale_log2);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32];
-          float sum = 0.f;
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = ex2(fmaf(s[2 * c + (e >> 4)][(2 * e) & 31], a.scale_log2, -ref));
-            const float y = ex2(fmaf(s[2 * c + (e >> 4)][(2 * e + 1) & 31], a.scale_log2, -ref));
-            sum += x + y;
-            r[e] = pack2<T>(x, y);
+          for (int e = 0; e < 16; ++e) {
+            float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, ref2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum[e & 1] = add2(sum[e & 1], x);
+            r[e] = pack2<T>(x.x, x.y);
           }
-          l += sum;
-          tmem_st_x32(S + c * 32, r);
+          tmem_st_x16(S + c * 16, r);
         }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.pfull[w]);
       }
       if (!ok) break;
+      if (more) {
+        if (!tiles) load_q();
+        q_ready();
+      }
       if (tiles) {
         if (!mbar_wait(&b.odone[w], oph, CH_WAIT)) {
           ok = false;
@@ -409,13 +529,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         oph ^= 1u;
         tc_fence_after();
       }
-      const bool whole = p.u0 == 0 && p.u1 == p.units;
-      float* mine =
-          whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.at == first ? 0 : 1)) * static_cast<int64_t>(SIZE);
       const int r = w * 128 + wr;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(p.q.start) + i) * a.heads + h) * D;
-      bool fine = true;
+      float2 odd2 = make_float2(0.f, 0.f);  // NaN as soon as one value is not finite
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -426,22 +542,26 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) fine = fine && fabsf(o[e]) < INFINITY;
+        for (int e = 0; e < 32; e += 2) odd2 = fma2(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), odd2);
         if (mine) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) mine[(c * 32 + e) * CH_ROWS + r] = o[e];
         } else if (in) {
+          uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint4 v;
-            v.x = pack2<T>(o[8 * e] * inv, o[8 * e + 1] * inv);
-            v.y = pack2<T>(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
-            v.z = pack2<T>(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
-            v.w = pack2<T>(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
-            reinterpret_cast<uint4*>(dst)[c * 4 + e] = v;
+          for (int e = 0; e < 16; ++e) v[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
+          // a row per lane: the wider the stores, the fewer lines they touch
+          if (wide) {
+            store32(dst + c * 32, v);
+            store32(dst + c * 32 + 16, v + 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
         }
       }
+      const bool fine = odd2.x + odd2.y == 0.f;
       if (mine) {
         mine[D * CH_ROWS + r] = m == -INFINITY ? m : m * a.scale_log2;
         mine[(D + 1) * CH_ROWS + r] = l;
@@ -458,13 +578,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         constexpr uint32_t ipv = instr_desc(FMT, false, true, 128, D);
         Ring<C::NST> ring;
         uint32_t qph = 0, pph = 0;  // phases, a bit per half
-        const uint32_t q0 = smem_u32(smem + C::QOFF), r0 = smem_u32(smem + C::RING);
+        const uint32_t q0 = desc_lo(smem_u32(smem + C::QOFF), 16), k0 = desc_lo(smem_u32(smem + C::RING), 16);
+        const uint32_t v0 = desc_lo(smem_u32(smem + C::RING), CH_KEYS * 128);
         auto qk = [&](int w, int st) {
+          const uint32_t qa = q0 + w * (C::TILE >> 4), kb = k0 + st * (C::TILE >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = static_cast<uint32_t>((k >> 2) * (CH_KEYS * 128) + (k & 3) * 32);
-            umma_f16(tmem + w * 128, smem_desc_sw128(q0 + w * C::TILE + off, 16, 1024),
-                     smem_desc_sw128(r0 + st * C::TILE + off, 16, 1024), iqk, k > 0 ? 1u : 0u);
+            const uint32_t off = static_cast<uint32_t>((k >> 2) * (CH_KEYS * 128) + (k & 3) * 32) >> 4;
+            umma_ss(tmem + w * 128, qa + off, kb + off, iqk, k > 0 ? 1u : 0u);
           }
           umma_commit(&b.sfull[w]);
         };
@@ -500,11 +621,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               if (w == 0) ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
               if (!ok) break;
               tc_fence_after();
+              const uint32_t vb = v0 + vst * (C::TILE >> 4);
 #pragma unroll
               for (int k = 0; k < CH_KEYS / 16; ++k)
-                umma_f16_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8,
-                            smem_desc_sw128(r0 + vst * C::TILE + k * 2048, CH_KEYS * 128, 1024), ipv,
-                            (j > 0 || k > 0) ? 1u : 0u);
+                umma_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, vb + k * (2048 >> 4), ipv, (j > 0 || k > 0) ? 1u : 0u);
               if (w == nw - 1) umma_commit(&b.empty[vst]);
               if (more) {
                 if (w == 0) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
@@ -527,14 +647,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       Ring<C::NRAW> raw;
       uint32_t zph = 0;
       int issued = 0;
-      const int box = min(1 << a.page_shift, CH_KEYS), boxes = CH_KEYS / box;
+      const int box = min(1 << a.page_shift, BITS == 16 ? CH_KEYS : CH_RAW), boxes = CH_KEYS / box;
       for (; p.at < p.end && ok; chunk_next(a, p)) {
         const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+        // a lane per box; the page of the next tile's box is looked up one tile ahead
+        auto find = [&](int key) { return key + lane * box < p.kend && lane < boxes ? key_at(a, p.s, p.head, key + lane * box) : 0; };
+        int64_t next = tiles ? find(p.u0 * CH_KEYS) : 0;
         for (int j = 0; j < tiles && ok; ++j) {
           const int key = (p.u0 + j) * CH_KEYS;
-          const int mykey = key + lane * box;
           const int n = min(boxes, (p.kend - key + box - 1) / box);  // boxes that hold keys
-          const int64_t at = lane < n ? key_at(a, p.s, p.head, mykey) : 0;
+          const int64_t at = next;
+          if (j + 1 < tiles) next = find(key + CH_KEYS);
           for (int kv = 0; kv < 2; ++kv) {
             if constexpr (BITS == 16) {
               if (!mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
@@ -570,21 +693,26 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               ++issued;
               ring.step();
             } else {
-              if (!mbar_wait(&b.rempty[raw.i], raw.ph ^ 1u, CH_WAIT)) {
-                ok = false;
-                break;
+              for (int hf = 0; hf < 2; ++hf) {
+                if (!mbar_wait(&b.rempty[raw.i], raw.ph ^ 1u, CH_WAIT)) {
+                  ok = false;
+                  break;
+                }
+                uint8_t* dst = smem + C::ROFF + raw.i * C::RAW;
+                const int b0 = hf * (boxes / 2), nb = max(0, min(boxes / 2, n - b0));
+                if (lane == 0) mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(nb * box * (C::ROW + 5)));
+                __syncwarp();
+                if (lane >= b0 && lane < b0 + nb) {
+                  const int x = (lane - b0) * box;
+                  const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.vc : a.kc) + at * C::ROW;
+                  bulk_load(dst + x * C::ROW, codes, box * C::ROW, &b.rfull[raw.i]);
+                  bulk_load(dst + CH_RAW * C::ROW + x * 4, (kv ? a.vs : a.ks) + at, box * 4, &b.rfull[raw.i]);
+                  bulk_load(dst + CH_RAW * (C::ROW + 4) + x, (kv ? a.vz : a.kz) + at, box, &b.rfull[raw.i]);
+                }
+                ++issued;
+                raw.step();
               }
-              uint8_t* dst = smem + C::ROFF + raw.i * C::RAW;
-              if (lane == 0) mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(n * box * (C::ROW + 5)));
-              __syncwarp();
-              if (lane < n) {
-                const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.vc : a.kc) + at * C::ROW;
-                bulk_load(dst + lane * box * C::ROW, codes, box * C::ROW, &b.rfull[raw.i]);
-                bulk_load(dst + CH_KEYS * C::ROW + lane * box * 4, (kv ? a.vs : a.ks) + at, box * 4, &b.rfull[raw.i]);
-                bulk_load(dst + CH_KEYS * (C::ROW + 4) + lane * box, (kv ? a.vz : a.kz) + at, box, &b.rfull[raw.i]);
-              }
-              ++issued;
-              raw.step();
+              if (!ok) break;
             }
           }
         }
@@ -616,60 +744,69 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
         for (int jj = 0; jj < 2 * tiles; ++jj) {
           const int rest = p.kend - (p.u0 + (jj >> 1)) * CH_KEYS;
-          if (!mbar_wait(&b.rfull[raw.i], raw.ph, CH_WAIT) || !mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
+          if (!mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
             ok = false;
             break;
           }
-          const uint8_t* src = smem + C::ROFF + raw.i * C::RAW;
-          uint8_t* dst = smem + C::RING + ring.i * C::TILE;
+          uint8_t* tile = smem + C::RING + ring.i * C::TILE;
+          constexpr int STEP = 128 / PPR, N = CH_RAW / STEP;  // rows between pieces, pieces of a thread
+          constexpr int WORDS = BITS / 2;                     // of a piece
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!mbar_wait(&b.rfull[raw.i], raw.ph, CH_WAIT)) {
+              ok = false;
+              break;
+            }
+            const uint8_t* src = smem + C::ROFF + raw.i * C::RAW;
+            uint8_t* dst = tile + hf * CH_RAW * 128;
+            const int left = rest - hf * CH_RAW;
+            uint32_t wd[N][WORDS];
+            float sc[N], zf[N];
 #pragma unroll
-          for (int x = 0; x < CH_KEYS * PPR / 128; ++x) {
-            const int r = r0 + x * (128 / PPR);
-            uint32_t out[8];
-            if (r < rest) {
-              const float s = *reinterpret_cast<const float*>(src + CH_KEYS * C::ROW + r * 4);
-              const float z = 8388608.f + static_cast<float>(src[CH_KEYS * (C::ROW + 4) + r]);
-              uint32_t wd[4];
-              if constexpr (BITS == 8) {
-                *reinterpret_cast<uint4*>(wd) = *reinterpret_cast<const uint4*>(src + r * C::ROW + col * 16);
+            for (int x = 0; x < N; ++x) {
+              const int r = r0 + x * STEP;
+              if constexpr (BITS == 8)
+                *reinterpret_cast<uint4*>(wd[x]) = *reinterpret_cast<const uint4*>(src + r * C::ROW + col * 16);
+              else
+                *reinterpret_cast<uint2*>(wd[x]) = *reinterpret_cast<const uint2*>(src + r * C::ROW + col * 8);
+              // rows past the last key: zeros
+              sc[x] = r < left ? *reinterpret_cast<const float*>(src + CH_RAW * C::ROW + r * 4) : 0.f;
+              zf[x] = __uint_as_float(0x4B000000u | src[CH_RAW * (C::ROW + 4) + r]);  // 2^23 + zero
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const uint32_t v = wd[e >> 1];
-                  const float f0 = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650u + (e & 1) * 2)) - z;
-                  const float f1 = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651u + (e & 1) * 2)) - z;
-                  out[e] = pack2<T>(s * f0, s * f1);
+            for (int x = 0; x < N; ++x) {
+              const float2 s2 = make_float2(sc[x], sc[x]), z2 = make_float2(-zf[x], -zf[x]);
+              uint32_t out[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float2 f;
+                if constexpr (BITS == 8) {
+                  const uint32_t v = wd[x][e >> 1];
+                  f.x = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650u + (e & 1) * 2));
+                  f.y = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651u + (e & 1) * 2));
+                } else {
+                  const uint32_t v = wd[x][e >> 2] >> ((e & 3) * 8);
+                  f.x = __uint_as_float((v & 15u) | 0x4B000000u);
+                  f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
                 }
-              } else {
-                *reinterpret_cast<uint2*>(wd) = *reinterpret_cast<const uint2*>(src + r * C::ROW + col * 8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const uint32_t v = wd[e >> 2] >> ((e & 3) * 8);
-                  const float f0 = __uint_as_float((v & 15u) | 0x4B000000u) - z;
-                  const float f1 = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u) - z;
-                  out[e] = pack2<T>(s * f0, s * f1);
-                }
+                f = mul2(add2(f, z2), s2);
+                out[e] = pack2<T>(f.x, f.y);
               }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) out[e] = 0;
+              // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
+              const int r = r0 + x * STEP;
+              const bool o = (col & 4) != 0;
+              const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
+              *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 1 : 0))) = o ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 0 : 1))) = o ? lo : hi;
             }
-            // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
-            const int o = col & 4 ? 1 : 0;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int hf = y ^ o;
-              *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + hf)) =
-                  hf ? make_uint4(out[4], out[5], out[6], out[7]) : make_uint4(out[0], out[1], out[2], out[3]);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.rempty[raw.i]);
+            raw.step();
           }
+          if (!ok) break;
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&b.full[ring.i]);
-            mbar_arrive(&b.rempty[raw.i]);
-          }
+          if (lane == 0) mbar_arrive(&b.full[ring.i]);
           ring.step();
-          raw.step();
         }
       }
     }
@@ -686,23 +823,25 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 
 // Joins the pieces of every tile that was cut: CTA c takes the tile that the border between shares c and
 // c + 1 cuts, unless an earlier border cuts it too.
-constexpr int CJ_THREADS = 256;
+constexpr int CJ_THREADS = CH_ROWS;
 template <typename T, int D>
 __global__ void __launch_bounds__(CJ_THREADS) chunk_join_kernel(const Args a, const Share sh, const float* __restrict__ part) {
   __shared__ int64_t plan[3];
   Piece p;
   int64_t per;
+  next_may_start();
   const int64_t c = static_cast<int64_t>(blockIdx.x) + 1;
   const bool any = chunk_first<CJ_THREADS>(a, sh, c, p, per, plan);
+  wait_for_last();
   if (!any || p.u0 == 0) return;
   const int64_t start = p.at - p.u0, end = start + p.units;
   if ((c - 1) * per > start) return;
   const int64_t c0 = c - 1, c1 = (end - 1) / per;
   constexpr int64_t SIZE = (D + 2) * CH_ROWS;
   const int rows = min(CH_ROWS, p.q.n * a.group - p.tile * CH_ROWS);
-  for (int e = threadIdx.x; e < (D / 8) * CH_ROWS; e += CJ_THREADS) {
-    const int r = e % CH_ROWS, col = (e / CH_ROWS) * 8;
-    if (r >= rows) continue;
+  // 8 columns per CTA of the second grid dimension, a row per thread
+  const int r = threadIdx.x, col = blockIdx.y * 8;
+  if (r < rows) {
     float m = -INFINITY, l = 0.f, v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -737,7 +876,9 @@ template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(128) chunk_redo_kernel(const Args a, const int* __restrict__ odd, int n) {
   const int lane = threadIdx.x & 31;
   int any = 0;
-  for (int x = threadIdx.x; x < n; x += 128) any |= __ldg(odd + x);
+  next_may_start();
+  wait_for_last();
+  for (int x = threadIdx.x; x < n; x += 128) any |= odd[x];
   if (!__syncthreads_or(any)) return;
   const int64_t all = static_cast<int64_t>(a.tokens) * a.heads;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); w < all; w += gridDim.x * 4) {
@@ -819,14 +960,11 @@ int run(const Args& a, cudaStream_t s) {
   int* odd = reinterpret_cast<int*>(static_cast<char*>(part) + pieces);
   chunk_kernel<T, D, BITS><<<sh.grid, C::THREADS, C::SMEM, s>>>(tk, tv, a, sh, static_cast<float*>(part), odd);
   int st = after_launch();
-  if (st == GPTQ_OK && sh.grid > 1) {
-    chunk_join_kernel<T, D><<<sh.grid - 1, CJ_THREADS, 0, s>>>(a, sh, static_cast<const float*>(part));
-    st = after_launch();
-  }
-  if (st == GPTQ_OK) {
-    chunk_redo_kernel<T, D, BITS><<<sh.grid, 128, 0, s>>>(a, odd, sh.grid);
-    st = after_launch();
-  }
+  if (st == GPTQ_OK && sh.grid > 1)
+    st = launch_next(chunk_join_kernel<T, D>, dim3(sh.grid - 1, D / 8), CJ_THREADS, 0, s, a, sh,
+                     static_cast<const float*>(part));
+  if (st == GPTQ_OK)
+    st = launch_next(chunk_redo_kernel<T, D, BITS>, dim3(sh.grid), 128, 0, s, a, static_cast<const int*>(odd), sh.grid);
   pool_free(part, s);
   return st;
 }

@@ -151,10 +151,13 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
   float* red_l = red_m + 4 * 16;
   __shared__ Cursor cur_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;");
+  next_may_start();
 
   Cursor cur;
-  if (!first_piece<ST_THREADS>(a, sh, ST_UNIT, cur, &cur_s)) return;
+  if (!first_piece<ST_THREADS>(a, sh, ST_UNIT, cur, &cur_s)) {
+    wait_for_last();
+    return;
+  }
   const int64_t first = cur.at;
   for (; cur.at < cur.end; next_piece(a, sh, ST_UNIT, cur)) {
     const Seq q = sequence(a, cur.s);
@@ -460,6 +463,7 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
     }
     __syncthreads();
   }
+  wait_for_last();
 }
 
 // Joins the pieces of every (sequence, kv head) that was cut.
@@ -469,8 +473,9 @@ __global__ void __launch_bounds__(ST_THREADS) step_join_kernel(const Args a, con
   const Seq q = sequence(a, s);
   const int rows = q.n * a.group;
   int64_t at, per;
+  next_may_start();
   const int64_t units = piece_line<ST_THREADS>(a, sh, ST_UNIT, s, at, per);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_last();
   if (units == 0) return;
   at += h * units;
   const int64_t c0 = at / per, c1 = (at + units - 1) / per;
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(ST_THREADS) step_join_kernel(const Args a, con
 }
 
 template <typename T, int D, int BITS>
-int run(const Args& a, cudaStream_t s) {
+int run(const Args& a, bool next, cudaStream_t s) {
   constexpr int smem = (4 * 16 * D + 2 * 4 * 16) * static_cast<int>(sizeof(float));
   const void* kern = reinterpret_cast<const void*>(step_kernel<T, D, BITS>);
   GPTQ_TRY(ensure_smem_limit(kern, smem));
@@ -526,24 +531,17 @@ int run(const Args& a, cudaStream_t s) {
     GPTQ_TRY(pool_alloc(&w, static_cast<size_t>(sh.grid) * 2 * 16 * (D + 2) * sizeof(float), s));
     part = static_cast<float*>(w);
   }
-  step_kernel<T, D, BITS><<<sh.grid, ST_THREADS, smem, s>>>(a, sh, part);
-  int st = after_launch();
+  int st;
+  if (next) {
+    st = launch_next(step_kernel<T, D, BITS>, dim3(sh.grid), ST_THREADS, smem, s, a, sh, part);
+  } else {
+    step_kernel<T, D, BITS><<<sh.grid, ST_THREADS, smem, s>>>(a, sh, part);
+    st = after_launch();
+  }
   if (!sh.whole) {
-    if (st == GPTQ_OK) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(a.seqs, a.kv_heads);
-      cfg.blockDim = dim3(ST_THREADS);
-      cfg.stream = s;
-      cudaLaunchAttribute at[1];  // may start (and plan) while the first launch drains; waits for it itself
-      at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      at[0].val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      if (cudaLaunchKernelEx(&cfg, step_join_kernel<T, D>, a, sh, static_cast<const float*>(part)) != cudaSuccess)
-        st = GPTQ_ERR_CUDA;
-      else
-        st = after_launch();
-    }
+    if (st == GPTQ_OK)
+      st = launch_next(step_join_kernel<T, D>, dim3(a.seqs, a.kv_heads), ST_THREADS, 0, s, a, sh,
+                       static_cast<const float*>(part));
     pool_free(part, s);
   }
   return st;
@@ -551,9 +549,9 @@ int run(const Args& a, cudaStream_t s) {
 
 }  // namespace
 
-int run_step(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s) {
+int run_step(const Args& a, int dtype, int head_dim, int bits, bool next, cudaStream_t s) {
 #define GPTQ_STEP(T, D)                                                                                    \
-  return bits == 16 ? run<T, D, 16>(a, s) : bits == 8 ? run<T, D, 8>(a, s) : run<T, D, 4>(a, s)
+  return bits == 16 ? run<T, D, 16>(a, next, s) : bits == 8 ? run<T, D, 8>(a, next, s) : run<T, D, 4>(a, next, s)
   if (dtype == GPTQ_BF16) {
     if (head_dim == 128) GPTQ_STEP(__nv_bfloat16, 128);
     GPTQ_STEP(__nv_bfloat16, 64);
