@@ -69,7 +69,7 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_of(const Args& a, const Seq& q, int tile) {
   Tile t;
-  const int last = min(q.n - 1, static_cast<int>((static_cast<int64_t>(tile + 1) * CH_ROWS - 1) / a.group));
+  const int last = min(q.n - 1, static_cast<int>((static_cast<uint32_t>(tile + 1) * CH_ROWS - 1) / static_cast<uint32_t>(a.group)));
   t.kend = seen(a, q, last);
   t.units = max(1, (t.kend + CH_KEYS - 1) / CH_KEYS);
   return t;
@@ -230,6 +230,12 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Untiled copy global -> shared (16-byte aligned, a multiple of 16 bytes).
@@ -270,6 +276,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 d;
+  asm("sub.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -301,6 +314,50 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+// 2^x of a pair without the exponential unit: x = n + f, n the nearest integer (the low bits after adding
+// 1.5 2^23), |f| <= 1/2, 2^f by a degree-4 polynomial fitted to least relative error (2.6e-6), n added to
+// the exponent.  x below -126 counts as -126; NaN stays non-finite.
+__device__ __forceinline__ float2 exp2_pair(float2 x) {
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
+  const float2 r = add2(x, make_float2(12582912.f, 12582912.f));
+  const float2 f = sub2(x, sub2(r, make_float2(12582912.f, 12582912.f)));
+  float2 y = fma2(f, make_float2(0.009570102207f, 0.009570102207f), make_float2(0.055917862803f, 0.055917862803f));
+  y = fma2(y, f, make_float2(0.240247443318f, 0.240247443318f));
+  y = fma2(y, f, make_float2(0.693121790886f, 0.693121790886f));
+  y = fma2(y, f, make_float2(0.999999284744f, 0.999999284744f));
+  y.x = __int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23));
+  y.y = __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23));
+  return y;
+}
+
+// Probabilities 2^(s scale + ref) of a row's 128 scores into tensor memory as 16-bit pairs; returns their
+// sum.  With SPLIT a quarter of them goes through exp2_pair, so that the exponential unit (16 per cycle and
+// SM, 1024 cycles for 128 rows) is not what a half's turn waits for; a score of -infinity needs the unit.
+template <typename T, bool SPLIT>
+__device__ __forceinline__ float weights(const float (&s)[4][32], float scale, float ref, uint32_t dst) {
+  const float2 sc2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, ref2);
+      if (SPLIT && (e & 3) == 3) {
+        x = exp2_pair(x);
+      } else {
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+      }
+      sum[e & 1] = add2(sum[e & 1], x);
+      r[e] = pack2<T>(x.x, x.y);
+    }
+    tmem_st_x16(dst + c * 16, r);
+  }
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // Byte offset of 16-byte chunk c (8 elements) of row r in an operand tile: 64-element blocks of [128 rows]
@@ -463,7 +520,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) settled(s[c]);
         const int key = k0 + j * CH_KEYS;
-        if (key + CH_KEYS > least) {  // some row of the warp does not see all of these keys
+        const bool cut = key + CH_KEYS > least;
+        if (cut) {  // some row of the warp does not see all of these keys
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -495,22 +553,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        const float2 ref2 = make_float2(ref, ref), sc2 = make_float2(a.scale_log2, a.scale_log2);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, ref2);
-            x.x = ex2(x.x);
-            x.y = ex2(x.y);
-            sum[e & 1] = add2(sum[e & 1], x);
-            r[e] = pack2<T>(x.x, x.y);
-          }
-          tmem_st_x16(S + c * 16, r);
-        }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l += cut ? weights<T, false>(s, a.scale_log2, ref, S) : weights<T, true>(s, a.scale_log2, ref, S);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -573,74 +616,89 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     regs_fewer<BITS == 16 ? 72 : 40>();
     if (warp == 8) {
       // -------------------------------------------------------------- issue of the matrix products
-      if (lane == 0) {
-        constexpr uint32_t iqk = instr_desc(FMT, false, false, 128, CH_KEYS);
-        constexpr uint32_t ipv = instr_desc(FMT, false, true, 128, D);
-        Ring<C::NST> ring;
-        uint32_t qph = 0, pph = 0;  // phases, a bit per half
-        const uint32_t q0 = desc_lo(smem_u32(smem + C::QOFF), 16), k0 = desc_lo(smem_u32(smem + C::RING), 16);
-        const uint32_t v0 = desc_lo(smem_u32(smem + C::RING), CH_KEYS * 128);
-        auto qk = [&](int w, int st) {
-          const uint32_t qa = q0 + w * (C::TILE >> 4), kb = k0 + st * (C::TILE >> 4);
+      // The whole warp walks the loops and one elected lane issues: descriptors then stay in uniform
+      // registers (a product issues every 66 cycles; from a single lane's branch every 82, measured alone).
+      constexpr uint32_t iqk = instr_desc(FMT, false, false, 128, CH_KEYS);
+      constexpr uint32_t ipv = instr_desc(FMT, false, true, 128, D);
+      const bool lead = elect_one();
+      Ring<C::NST> ring;
+      uint32_t qph = 0, pph = 0;  // phases, a bit per half
+      const uint32_t q0 = desc_lo(smem_u32(smem + C::QOFF), 16), k0 = desc_lo(smem_u32(smem + C::RING), 16);
+      const uint32_t v0 = desc_lo(smem_u32(smem + C::RING), CH_KEYS * 128);
+      auto qk = [&](int w, int st) {
+        const uint32_t qa = q0 + w * (C::TILE >> 4), kb = k0 + st * (C::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = static_cast<uint32_t>((k >> 2) * (CH_KEYS * 128) + (k & 3) * 32) >> 4;
-            umma_ss(tmem + w * 128, qa + off, kb + off, iqk, k > 0 ? 1u : 0u);
-          }
-          umma_commit(&b.sfull[w]);
-        };
-        for (; p.at < p.end && ok; chunk_next(a, p)) {
-          const int rows = p.q.n * a.group;
-          const int nw = rows > p.tile * CH_ROWS + 128 ? 2 : 1;
-          const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
-          for (int w = 0; w < nw; ++w) {  // Q of this piece is in place, O of the last one is read
-            ok = ok && mbar_wait(&b.qfull[w], (qph >> w) & 1u, CH_WAIT);
-            qph ^= 1u << w;
-          }
-          if (!ok) break;
-          if (!tiles) continue;
-          if (!mbar_wait(&b.full[ring.i], ring.ph, CH_WAIT)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          for (int w = 0; w < nw; ++w) qk(w, ring.i);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = static_cast<uint32_t>((k >> 2) * (CH_KEYS * 128) + (k & 3) * 32) >> 4;
+          umma_ss(tmem + w * 128, qa + off, kb + off, iqk, k > 0 ? 1u : 0u);
+        }
+        umma_commit(&b.sfull[w]);
+      };
+      for (; p.at < p.end && ok; chunk_next(a, p)) {
+        const bool two = p.q.n * a.group > p.tile * CH_ROWS + 128;  // the tile has a second half
+        const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+        ok = mbar_wait(&b.qfull[0], qph & 1u, CH_WAIT);  // Q of this piece is in place
+        qph ^= 1u;
+        if (two) {
+          ok = ok && mbar_wait(&b.qfull[1], (qph >> 1) & 1u, CH_WAIT);
+          qph ^= 2u;
+        }
+        if (!ok) break;
+        if (!tiles) continue;
+        if (!mbar_wait(&b.full[ring.i], ring.ph, CH_WAIT)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lead) {
+          qk(0, ring.i);
+          if (two) qk(1, ring.i);
           umma_commit(&b.empty[ring.i]);
+        }
+        __syncwarp();
+        ring.step();
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int vst = ring.i;
+          const uint32_t vph = ring.ph;
           ring.step();
-          for (int j = 0; j < tiles && ok; ++j) {
-            const int vst = ring.i;
-            const uint32_t vph = ring.ph;
-            ring.step();
-            const int kst = ring.i;
-            const uint32_t kph = ring.ph;
-            const bool more = j + 1 < tiles;
-            if (more) ring.step();
-            for (int w = 0; w < nw; ++w) {
-              ok = ok && mbar_wait(&b.pfull[w], (pph >> w) & 1u, CH_WAIT);
-              pph ^= 1u << w;
-              if (w == 0) ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
-              if (!ok) break;
-              tc_fence_after();
+          const int kst = ring.i;
+          const uint32_t kph = ring.ph;
+          const bool more = j + 1 < tiles;
+          if (more) ring.step();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w == 1 && !two) break;
+            ok = ok && mbar_wait(&b.pfull[w], (pph >> w) & 1u, CH_WAIT);
+            pph ^= 1u << w;
+            if (w == 0) ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
+            if (!ok) break;
+            tc_fence_after();
+            const bool last = w == 1 || !two;  // half to use this tile of V, and of K
+            if (lead) {
               const uint32_t vb = v0 + vst * (C::TILE >> 4);
 #pragma unroll
               for (int k = 0; k < CH_KEYS / 16; ++k)
                 umma_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, vb + k * (2048 >> 4), ipv, (j > 0 || k > 0) ? 1u : 0u);
-              if (w == nw - 1) umma_commit(&b.empty[vst]);
-              if (more) {
-                if (w == 0) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
-                if (!ok) break;
-                tc_fence_after();
+              if (last) umma_commit(&b.empty[vst]);
+              if (!more) umma_commit(&b.odone[w]);
+            }
+            __syncwarp();
+            if (more) {
+              if (w == 0) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
+              if (!ok) break;
+              tc_fence_after();
+              if (lead) {
                 qk(w, kst);
-                if (w == nw - 1) umma_commit(&b.empty[kst]);
-              } else {
-                umma_commit(&b.odone[w]);
+                if (last) umma_commit(&b.empty[kst]);
               }
+              __syncwarp();
             }
           }
         }
-        umma_commit(b.done);
-        mbar_wait(b.done, 0, CH_WAIT);
       }
+      if (lead) umma_commit(b.done);
+      __syncwarp();
+      mbar_wait(b.done, 0, CH_WAIT);
     } else if (warp == 9) {
       // -------------------------------------------------------------- keys and values, page by page
       Ring<C::NST> ring;
