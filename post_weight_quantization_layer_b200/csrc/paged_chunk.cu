@@ -56,8 +56,9 @@ struct Cfg {
   static constexpr int RING = 2 * TILE;
   static constexpr int ROFF = RING + NST * TILE;
   static constexpr int BARS = ROFF + NRAW * RAW;
-  static constexpr int SMEM = BARS + 320 + 1024;
-  static_assert((2 * NST + 2 * NRAW + 10) * 8 + 4 <= 320, "barriers");
+  static constexpr int NBARS = 2 * NST + 2 * NRAW + 16;
+  static constexpr int JOBS = BARS + NBARS * 8 + 8;
+  static constexpr int SMEM = JOBS + 2 * 40 + 1024;
   static_assert(SMEM + 160 <= 232448, "shared memory of a CTA");
 };
 
@@ -276,13 +277,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-  float2 d;
-  asm("sub.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -316,28 +310,13 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
-// 2^x of a pair without the exponential unit: x = n + f, n the nearest integer (the low bits after adding
-// 1.5 2^23), |f| <= 1/2, 2^f by a degree-4 polynomial fitted to least relative error (2.6e-6), n added to
-// the exponent.  x below -126 counts as -126; NaN stays non-finite.
-__device__ __forceinline__ float2 exp2_pair(float2 x) {
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
-  const float2 r = add2(x, make_float2(12582912.f, 12582912.f));
-  const float2 f = sub2(x, sub2(r, make_float2(12582912.f, 12582912.f)));
-  float2 y = fma2(f, make_float2(0.009570102207f, 0.009570102207f), make_float2(0.055917862803f, 0.055917862803f));
-  y = fma2(y, f, make_float2(0.240247443318f, 0.240247443318f));
-  y = fma2(y, f, make_float2(0.693121790886f, 0.693121790886f));
-  y = fma2(y, f, make_float2(0.999999284744f, 0.999999284744f));
-  y.x = __int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23));
-  y.y = __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23));
-  return y;
-}
-
 // Probabilities 2^(s scale + ref) of a row's 128 scores into tensor memory as 16-bit pairs; returns their
-// sum.  With SPLIT a quarter of them goes through exp2_pair, so that the exponential unit (16 per cycle and
-// SM, 1024 cycles for 128 rows) is not what a half's turn waits for; a score of -infinity needs the unit.
-template <typename T, bool SPLIT>
-__device__ __forceinline__ float weights(const float (&s)[4][32], float scale, float ref, uint32_t dst) {
+// sum; arrives at `most` and `full` as they get there.  All go through the exponential unit: a share of
+// them by polynomial was faster alone (959 cycles instead of 1168 for a warp with three of eight) and
+// slower here (prompts of 2048, 32 heads: 244 us instead of 223), where registers are short.
+template <typename T>
+__device__ __forceinline__ float weights(const float (&s)[4][32], float scale, float ref, uint32_t dst, uint64_t* most,
+                                         uint64_t* full) {
   const float2 sc2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -346,16 +325,18 @@ __device__ __forceinline__ float weights(const float (&s)[4][32], float scale, f
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, ref2);
-      if (SPLIT && (e & 3) == 3) {
-        x = exp2_pair(x);
-      } else {
-        x.x = ex2(x.x);
-        x.y = ex2(x.y);
-      }
+      x.x = ex2(x.x);
+      x.y = ex2(x.y);
       sum[e & 1] = add2(sum[e & 1], x);
       r[e] = pack2<T>(x.x, x.y);
     }
     tmem_st_x16(dst + c * 16, r);
+    if (c >= 2) {  // the first 96 keys may be multiplied while the last are on their way
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(c == 2 ? most : full);
+    }
   }
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -367,7 +348,43 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 }
 
 struct Bars {
-  uint64_t *full, *empty, *rfull, *rempty, *qfull, *sfull, *pfull, *odone, *zero, *done;
+  uint64_t *full, *empty, *rfull, *rempty, *jfull, *jempty, *qfull, *sfull, *pmost, *pfull, *odone, *zero, *done;
+};
+
+// What the other warps have to know of a piece, as the warp that walks the line tells them through shared
+// memory (two entries in turn): they then keep little of it in registers.
+struct Job {
+  int start, n, len;  // the sequence
+  int head, tile;
+  int key0, kend;     // keys of the piece
+  int tiles;          // of CH_KEYS keys; -1: no piece is left
+  int slot;           // where the part is left behind: 0 or 1 of the CTA; -1: the tile is whole
+  int pad;
+};
+static_assert(sizeof(Job) == 40, "Job");
+
+// A reader's side of the jobs: waits for the next one, takes a copy and gives the entry back.
+struct JobReader {
+  const Job* jobs;
+  uint64_t *full, *empty;
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ JobReader(const Job* j, const Bars& b) : jobs(j), full(b.jfull), empty(b.jempty) {}
+  // false where the wait ran out (job.tiles is then -1)
+  __device__ __forceinline__ bool next(Job& job) {
+    const bool there = mbar_wait(&full[i], ph, CH_WAIT);
+    if (there)
+      job = jobs[i];
+    else
+      job.tiles = -1;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[i]);
+    if (++i == 2) {
+      i = 0;
+      ph ^= 1u;
+    }
+    return there;
+  }
 };
 
 // A place in a ring of N: index and phase.
@@ -411,13 +428,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   b.empty = b.full + C::NST;
   b.rfull = b.empty + C::NST;
   b.rempty = b.rfull + C::NRAW;
-  b.qfull = b.rempty + C::NRAW;
+  b.jfull = b.rempty + C::NRAW;
+  b.jempty = b.jfull + 2;
+  b.qfull = b.jempty + 2;
   b.sfull = b.qfull + 2;
-  b.pfull = b.sfull + 2;
+  b.pmost = b.sfull + 2;
+  b.pfull = b.pmost + 2;
   b.odone = b.pfull + 2;
   b.zero = b.odone + 2;
   b.done = b.zero + 1;
   uint32_t* slot = reinterpret_cast<uint32_t*>(b.done + 1);
+  Job* jobs = reinterpret_cast<Job*>(smem + C::JOBS);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&b.full[i], BITS == 16 ? 1 : 4);
@@ -428,8 +449,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       mbar_init(&b.rempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.jfull[i], 1);
+      mbar_init(&b.jempty[i], BITS == 16 ? 9 : 13);  // softmax, issuing and converting warps
       mbar_init(&b.qfull[i], 4);
       mbar_init(&b.sfull[i], 1);
+      mbar_init(&b.pmost[i], 4);
       mbar_init(&b.pfull[i], 4);
       mbar_init(&b.odone[i], 1);
     }
@@ -458,16 +482,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     // a row of the tile, counted from the first token that the tile touches, is token r / group of it
     const uint32_t recip = 65536u / a.group + 1u;  // r < 320: (r * recip) >> 16 is exact
-    auto absent = [&]() { return p.tile * CH_ROWS + w * 128 >= p.q.n * a.group; };  // the tile has no such half
-    auto skip = [&]() {
-      while (p.at < p.end && absent()) chunk_next(a, p);
-      return p.at < p.end;
+    JobReader reader(jobs, b);
+    Job job;
+    auto next_job = [&]() {  // the next piece whose tile has this half
+      do {
+        if (!reader.next(job)) ok = false;
+      } while (job.tiles >= 0 && job.tile * CH_ROWS + w * 128 >= job.n * a.group);
+      return job.tiles >= 0;
     };
-    // Q of this half of the piece p, 16 bytes a lane along the rows; rows past the last are zeros
+    // Q of this half of the piece, 16 bytes a lane along the rows; rows past the last are zeros
     auto load_q = [&]() {
-      const int row0 = p.tile * CH_ROWS, i0 = row0 / a.group, over = row0 - i0 * a.group;
-      const int rows = p.q.n * a.group - row0 - w * 128;
-      const T* base = static_cast<const T*>(a.q) + (p.q.start + i0) * a.q_ts + p.head * a.group * a.q_hs;
+      const uint32_t row0 = job.tile * CH_ROWS, i0 = row0 / static_cast<uint32_t>(a.group), over = row0 - i0 * a.group;
+      const int rows = job.n * a.group - static_cast<int>(row0) - w * 128;
+      const T* base = static_cast<const T*>(a.q) + (job.start + i0) * a.q_ts + job.head * a.group * a.q_hs;
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) {
         const int e = x * 128 + (threadIdx.x & 127), r = e / (D / 8), c = e % (D / 8);
@@ -484,44 +511,42 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.qfull[w]);
     };
-    bool more = skip();
+    bool more = next_job();
     if (more) {
       load_q();
       q_ready();
     }
     while (more) {
-      const int row = p.tile * CH_ROWS + w * 128 + wr;
-      const bool in = row < p.q.n * a.group;
-      const int i = in ? row / a.group : 0, h = p.head * a.group + (in ? row - i * a.group : 0);
-      const int k0 = p.u0 * CH_KEYS, k1 = min(p.u1 * CH_KEYS, p.kend);
-      const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
-      const int see = in ? min(k1, seen(a, p.q, i)) : k1;  // rows past the last: whatever comes out is not used
+      const int row = job.tile * CH_ROWS + w * 128 + wr;
+      const bool in = row < job.n * a.group;
+      const uint32_t row0 = job.tile * CH_ROWS, t0 = row0 / static_cast<uint32_t>(a.group);
+      const uint32_t rr = row - t0 * a.group, ti = (rr * recip) >> 16;
+      const int i = in ? t0 + ti : 0, h = job.head * a.group + (in ? rr - ti * a.group : 0);
+      const int tiles = job.tiles;
+      int key = job.key0;
+      const Seq q{job.start, job.n, job.len};
+      const int see = in ? min(job.kend, seen(a, q, i)) : job.kend;  // rows past the last: what comes out is not used
       int least = see;
       for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-      const bool whole = p.u0 == 0 && p.u1 == p.units;
-      float* mine =
-          whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.at == first ? 0 : 1)) * static_cast<int64_t>(SIZE);
-      T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(p.q.start) + i) * a.heads + h) * D;
-      chunk_next(a, p);
-      more = skip();
+      float* mine = job.slot < 0 ? nullptr
+                                 : part + (static_cast<int64_t>(blockIdx.x) * 2 + job.slot) * static_cast<int64_t>(SIZE) +
+                                       w * 128 + wr;
+      T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(job.start) + i) * a.heads + h) * D;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < tiles; ++j) {
+      for (int j = 0; j < tiles; ++j, key += CH_KEYS) {
         if (!mbar_wait(&b.sfull[w], sph, CH_WAIT)) {
           ok = false;
           break;
         }
         sph ^= 1u;
         tc_fence_after();
-        if (j + 1 == tiles && more) load_q();  // the last scores are there: Q's place is free for the next piece's
         float s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_x32_nowait(S + c * 32, s[c]);
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 4; ++c) settled(s[c]);
-        const int key = k0 + j * CH_KEYS;
-        const bool cut = key + CH_KEYS > least;
-        if (cut) {  // some row of the warp does not see all of these keys
+        if (key + CH_KEYS > least) {  // some row of the warp does not see all of these keys
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -553,17 +578,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        l += cut ? weights<T, false>(s, a.scale_log2, ref, S) : weights<T, true>(s, a.scale_log2, ref, S);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.pfull[w]);
+        l += weights<T>(s, a.scale_log2, ref, S, &b.pmost[w], &b.pfull[w]);
+        if (j + 1 == tiles) {  // the last scores were there: Q's place is free for the next piece's
+          more = next_job();
+          if (more) load_q();
+        }
       }
       if (!ok) break;
-      if (more) {
-        if (!tiles) load_q();
-        q_ready();
+      if (!tiles) {
+        more = next_job();
+        if (more) load_q();
       }
+      if (more) q_ready();
       if (tiles) {
         if (!mbar_wait(&b.odone[w], oph, CH_WAIT)) {
           ok = false;
@@ -572,7 +598,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         oph ^= 1u;
         tc_fence_after();
       }
-      const int r = w * 128 + wr;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float2 odd2 = make_float2(0.f, 0.f);  // NaN as soon as one value is not finite
 #pragma unroll
@@ -588,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         for (int e = 0; e < 32; e += 2) odd2 = fma2(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), odd2);
         if (mine) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mine[(c * 32 + e) * CH_ROWS + r] = o[e];
+          for (int e = 0; e < 32; ++e) mine[(c * 32 + e) * CH_ROWS] = o[e];
         } else if (in) {
           uint32_t v[16];
 #pragma unroll
@@ -606,8 +631,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       }
       const bool fine = odd2.x + odd2.y == 0.f;
       if (mine) {
-        mine[D * CH_ROWS + r] = m == -INFINITY ? m : m * a.scale_log2;
-        mine[(D + 1) * CH_ROWS + r] = l;
+        mine[D * CH_ROWS] = m == -INFINITY ? m : m * a.scale_log2;
+        mine[(D + 1) * CH_ROWS] = l;
       }
       tc_fence_before();
       if (in && !fine) any_odd = 1;
@@ -634,9 +659,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         umma_commit(&b.sfull[w]);
       };
-      for (; p.at < p.end && ok; chunk_next(a, p)) {
-        const bool two = p.q.n * a.group > p.tile * CH_ROWS + 128;  // the tile has a second half
-        const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+      JobReader reader(jobs, b);
+      Job job;
+      while (ok) {
+        ok = reader.next(job);
+        if (job.tiles < 0) break;
+        const bool two = job.n * a.group > job.tile * CH_ROWS + 128;  // the tile has a second half
+        const int tiles = job.tiles;
         ok = mbar_wait(&b.qfull[0], qph & 1u, CH_WAIT);  // Q of this piece is in place
         qph ^= 1u;
         if (two) {
@@ -668,31 +697,38 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (w == 1 && !two) break;
-            ok = ok && mbar_wait(&b.pfull[w], (pph >> w) & 1u, CH_WAIT);
-            pph ^= 1u << w;
-            if (w == 0) ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
+            if (w == 0) {
+              ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
+              if (more) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
+            }
+            const bool last = w == 1 || !two;  // half to use this tile of V, and of K
+            const uint32_t vb = v0 + vst * (C::TILE >> 4);
+            ok = ok && mbar_wait(&b.pmost[w], (pph >> w) & 1u, CH_WAIT);
             if (!ok) break;
             tc_fence_after();
-            const bool last = w == 1 || !two;  // half to use this tile of V, and of K
             if (lead) {
-              const uint32_t vb = v0 + vst * (C::TILE >> 4);
 #pragma unroll
-              for (int k = 0; k < CH_KEYS / 16; ++k)
+              for (int k = 0; k < 6; ++k)
                 umma_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, vb + k * (2048 >> 4), ipv, (j > 0 || k > 0) ? 1u : 0u);
-              if (last) umma_commit(&b.empty[vst]);
-              if (!more) umma_commit(&b.odone[w]);
             }
             __syncwarp();
-            if (more) {
-              if (w == 0) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
-              if (!ok) break;
-              tc_fence_after();
-              if (lead) {
+            ok = mbar_wait(&b.pfull[w], (pph >> w) & 1u, CH_WAIT);
+            pph ^= 1u << w;
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+              for (int k = 6; k < CH_KEYS / 16; ++k)
+                umma_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, vb + k * (2048 >> 4), ipv, 1u);
+              if (last) umma_commit(&b.empty[vst]);
+              if (more) {
                 qk(w, kst);
                 if (last) umma_commit(&b.empty[kst]);
+              } else {
+                umma_commit(&b.odone[w]);
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
         }
       }
@@ -706,8 +742,26 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       uint32_t zph = 0;
       int issued = 0;
       const int box = min(1 << a.page_shift, BITS == 16 ? CH_KEYS : CH_RAW), boxes = CH_KEYS / box;
+      int ji = 0;
+      uint32_t jph = 1u;
+      auto tell = [&](const Job& job) {
+        if (!mbar_wait(&b.jempty[ji], jph, CH_WAIT)) return false;
+        if (lane == 0) {
+          jobs[ji] = job;
+          mbar_arrive(&b.jfull[ji]);
+        }
+        __syncwarp();
+        if (++ji == 2) {
+          ji = 0;
+          jph ^= 1u;
+        }
+        return true;
+      };
       for (; p.at < p.end && ok; chunk_next(a, p)) {
         const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
+        const bool whole = p.u0 == 0 && p.u1 == p.units;
+        ok = tell(Job{p.q.start, p.q.n, p.q.len, p.head, p.tile, p.u0 * CH_KEYS, min(p.u1 * CH_KEYS, p.kend), tiles,
+                      whole ? -1 : (p.at == first ? 0 : 1), 0});
         // a lane per box; the page of the next tile's box is looked up one tile ahead
         auto find = [&](int key) { return key + lane * box < p.kend && lane < boxes ? key_at(a, p.s, p.head, key + lane * box) : 0; };
         int64_t next = tiles ? find(p.u0 * CH_KEYS) : 0;
@@ -775,6 +829,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
       }
+      if (ok) ok = tell(Job{0, 0, 0, 0, 0, 0, 0, -1, 0, 0});
       // no copy of ours may still be landing in shared memory when the CTA leaves
       if (!ok) {
         constexpr int N = BITS == 16 ? C::NST : C::NRAW;
@@ -798,10 +853,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       const int col = tid % PPR, r0 = tid / PPR;
       Ring<C::NST> ring;
       Ring<C::NRAW> raw;
-      for (; p.at < p.end && ok; chunk_next(a, p)) {
-        const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
-        for (int jj = 0; jj < 2 * tiles; ++jj) {
-          const int rest = p.kend - (p.u0 + (jj >> 1)) * CH_KEYS;
+      JobReader reader(jobs, b);
+      Job job;
+      while (ok) {
+        ok = reader.next(job);
+        if (job.tiles < 0) break;
+        for (int jj = 0; jj < 2 * job.tiles; ++jj) {
+          const int rest = job.kend - job.key0 - (jj >> 1) * CH_KEYS;
           if (!mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
             ok = false;
             break;
