@@ -8,7 +8,7 @@
 // other half.  512 columns of tensor memory: two S (128 each, P over them), two O (head_dim each).
 //
 //  * Roles: warps 0-3 and 4-7 softmax, rescaling and output of their half; warp 8 issues the matrix
-//    products; warp 9 brings keys and values; warps 12-15 (8- and 4-bit caches only) turn codes into
+//    products; warp 9 brings keys and values; warps 12-19 (8- and 4-bit caches only) turn codes into
 //    16-bit operands.  Registers move from the last two to the first.
 //  * 16-bit pages come by TMA straight into the swizzled operand tiles.  Pages of codes come by bulk
 //    copies (codes, scales and zeros of a page and head are contiguous) into a staging ring, from
@@ -45,13 +45,14 @@ __device__ int g_chunk_status = 0;
 
 template <int D, int BITS>
 struct Cfg {
-  static constexpr int THREADS = BITS == 16 ? 384 : 512;
+  static constexpr int CONV = BITS == 16 ? 0 : 256;     // converting threads
+  static constexpr int THREADS = 384 + CONV;
   static constexpr int TILE = CH_KEYS * D * 2;         // bytes of an operand tile
   static constexpr int NST = D == 128 ? 4 : 6;         // operand tiles in the ring
   static constexpr int ROW = D * BITS / 8;
   // staging of codes, scales and zeros, half a tile of keys each
   static constexpr int RAW = BITS == 16 ? 0 : ((CH_RAW * (ROW + 5) + 127) / 128) * 128;
-  static constexpr int NRAW = BITS == 16 ? 1 : (BITS == 8 ? 4 : 6);
+  static constexpr int NRAW = BITS == 16 ? 1 : 4;      // two halves of keys, two of values
   static constexpr int QOFF = 0;
   static constexpr int RING = 2 * TILE;
   static constexpr int ROFF = RING + NST * TILE;
@@ -59,7 +60,7 @@ struct Cfg {
   static constexpr int NBARS = 2 * NST + 2 * NRAW + 16;
   static constexpr int JOBS = BARS + NBARS * 8 + 8;
   static constexpr int SMEM = JOBS + 2 * 40 + 1024;
-  static_assert(SMEM + 160 <= 232448, "shared memory of a CTA");
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 // ------------------------------------------------------------------ the line of units
@@ -103,12 +104,12 @@ __device__ __forceinline__ void enter_tile(const Args& a, Piece& p, int u0) {
   p.u1 = static_cast<int>(min(static_cast<int64_t>(t.units), u0 + (p.end - p.at)));
 }
 
-// The piece at position `start` of the line for a CTA whose share ends at `end`.  All threads.
+// The first piece of share `cta`; false where it is empty.  All threads; shared: 3 + THREADS / 32 words.
 template <int THREADS>
 __device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& p, int64_t& per, int64_t* shared) {
   int64_t all = 0, total;
   for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += head_units(a, x);
-  block_scan<THREADS>(all, total);
+  block_scan<THREADS>(all, total, shared + 3);
   total *= a.kv_heads;
   per = share_of(sh, total);
   p.at = cta * per;
@@ -119,7 +120,7 @@ __device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& 
     const int x = x0 + threadIdx.x;
     const int64_t u = x < a.seqs ? head_units(a, x) * a.kv_heads : 0;
     int64_t sum;
-    const int64_t incl = block_scan<THREADS>(u, sum);
+    const int64_t incl = block_scan<THREADS>(u, sum, shared + 3);
     const int64_t lo = base + incl - u;
     if (u && lo <= p.at && p.at < lo + u) {
       shared[0] = x;
@@ -310,26 +311,53 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
-// Probabilities 2^(s scale + ref) of a row's 128 scores into tensor memory as 16-bit pairs; returns their
-// sum; arrives at `most` and `full` as they get there.  All go through the exponential unit: a share of
-// them by polynomial was faster alone (959 cycles instead of 1168 for a warp with three of eight) and
-// slower here (prompts of 2048, 32 heads: 244 us instead of 223), where registers are short.
-template <typename T>
-__device__ __forceinline__ float weights(const float (&s)[4][32], float scale, float ref, uint32_t dst, uint64_t* most,
-                                         uint64_t* full) {
+// Scores of keys (from `key`) that the row does not see become -infinity.
+__device__ __forceinline__ void hide(float (&x)[32], int key, int see) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) x[e] = key + e < see ? x[e] : -INFINITY;
+}
+
+template <int N>
+__device__ __forceinline__ float highest(const float (&x)[N][32]) {
+  float m[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) m[c] = fmaxf(x[0][c], x[0][c + 8]);
+#pragma unroll
+  for (int y = 16; y < N * 32; y += 16)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) m[c] = max3(m[c], x[y >> 5][(y & 31) + c], x[y >> 5][(y & 31) + c + 8]);
+  return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+
+// Probabilities 2^(score scale + ref) of a row's 128 scores into tensor memory as 16-bit pairs, over the
+// scores: part c of 32 keys takes columns that part c / 2 has left.  x holds the first parts, the others are
+// read again.  Returns the sum; arrives at `most` and `full` as they get there.  All go through the
+// exponential unit: a share of them by polynomial was faster alone (959 cycles instead of 1168 for a warp
+// with three of eight) and slower here (prompts of 2048, 32 heads: 244 us instead of 223), where its
+// registers and issue slots are missed.
+template <typename T, int KEEP>
+__device__ __forceinline__ float weights(float (&x)[KEEP][32], float scale, float ref, uint32_t dst, int key, int see,
+                                         int least, uint64_t* most, uint64_t* full) {
   const float2 sc2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
+    float(&v)[32] = x[c % KEEP];
+    if (c >= KEEP) {
+      tmem_ld_wait();
+      settled(v);
+      if (key + CH_KEYS > least) hide(v, key + c * 32, see);
+    }
     uint32_t r[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, ref2);
-      x.x = ex2(x.x);
-      x.y = ex2(x.y);
-      sum[e & 1] = add2(sum[e & 1], x);
-      r[e] = pack2<T>(x.x, x.y);
+      float2 p = fma2(make_float2(v[2 * e], v[2 * e + 1]), sc2, ref2);
+      p.x = ex2(p.x);
+      p.y = ex2(p.y);
+      sum[e & 1] = add2(sum[e & 1], p);
+      r[e] = pack2<T>(p.x, p.y);
     }
+    if (c + KEEP < 4) tmem_ld_x32_nowait(dst + (c + KEEP) * 32, v);
     tmem_st_x16(dst + c * 16, r);
     if (c >= 2) {  // the first 96 keys may be multiplied while the last are on their way
       tmem_st_wait();
@@ -406,17 +434,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                  const Share sh, float* __restrict__ part, int* __restrict__ odd) {
   using C = Cfg<D, BITS>;
   constexpr int SIZE = (D + 2) * CH_ROWS;  // floats of a piece left behind
+  constexpr int KEEP = BITS == 16 ? 4 : 1;
   constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0u : 1u;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ int64_t plan[3];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Piece p;
   int64_t per;
-  __shared__ int any_odd;
   next_may_start();
-  if (threadIdx.x == 0) any_odd = 0;
-  if (!chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, plan)) {
+  // (the operand ring is not in use yet)
+  if (!chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem))) {
     if (threadIdx.x == 0) odd[blockIdx.x] = 0;
     return;
   }
@@ -438,6 +465,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   b.zero = b.odone + 2;
   b.done = b.zero + 1;
   uint32_t* slot = reinterpret_cast<uint32_t*>(b.done + 1);
+  int* any_odd = reinterpret_cast<int*>(slot + 1);
   Job* jobs = reinterpret_cast<Job*>(smem + C::JOBS);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
@@ -450,13 +478,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.jfull[i], 1);
-      mbar_init(&b.jempty[i], BITS == 16 ? 9 : 13);  // softmax, issuing and converting warps
+      mbar_init(&b.jempty[i], 9 + C::CONV / 32);  // softmax, issuing and converting warps
       mbar_init(&b.qfull[i], 4);
       mbar_init(&b.sfull[i], 1);
       mbar_init(&b.pmost[i], 4);
       mbar_init(&b.pfull[i], 4);
       mbar_init(&b.odone[i], 1);
     }
+    *any_odd = 0;
     mbar_init(b.zero, 1);
     mbar_init(b.done, 1);
     fence_barrier_init();
@@ -473,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax, one thread per row
-    regs_more<BITS == 16 ? 216 : 200>();
+    regs_more<BITS == 16 ? 216 : 120>();
     const int w = warp >> 2, wr = (warp & 3) * 32 + lane;  // half, row of the half
     uint8_t* qs = smem + C::QOFF + w * C::TILE;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -540,26 +569,23 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         sph ^= 1u;
         tc_fence_after();
-        float s[4][32];
+        // The maximum first, then the probabilities: only KEEP of the four 32-key parts of the scores stay in
+        // registers between the two, the others are read from tensor memory again.
+        float x[KEEP][32];
+        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32_nowait(S + c * 32, s[c]);
-        tmem_ld_wait();
+        for (int c = 4 - KEEP; c >= 0; c -= KEEP) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) settled(s[c]);
-        if (key + CH_KEYS > least) {  // some row of the warp does not see all of these keys
+          for (int y = 0; y < KEEP; ++y) tmem_ld_x32_nowait(S + (c + y) * 32, x[y]);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int y = 0; y < KEEP; ++y) settled(x[y]);
+          if (key + CH_KEYS > least) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[c][e] = key + c * 32 + e < see ? s[c][e] : -INFINITY;
+            for (int y = 0; y < KEEP; ++y) hide(x[y], key + (c + y) * 32, see);
+          }
+          top = fmaxf(top, highest(x));
         }
-        float mx[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mx[c] = fmaxf(s[0][c], s[0][c + 8]);
-#pragma unroll
-        for (int x = 16; x < 128; x += 16)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) mx[c] = max3(mx[c], s[x >> 5][(x & 31) + c], s[x >> 5][(x & 31) + c + 8]);
-        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
         if (j == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, (top - m) * a.scale_log2 > CH_GROW)) {
@@ -578,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        l += weights<T>(s, a.scale_log2, ref, S, &b.pmost[w], &b.pfull[w]);
+        l += weights<T, KEEP>(x, a.scale_log2, ref, S, key, see, least, &b.pmost[w], &b.pfull[w]);
         if (j + 1 == tiles) {  // the last scores were there: Q's place is free for the next piece's
           more = next_job();
           if (more) load_q();
@@ -635,10 +661,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         mine[(D + 1) * CH_ROWS] = l;
       }
       tc_fence_before();
-      if (in && !fine) any_odd = 1;
+      if (in && !fine) *any_odd = 1;
     }
   } else if (warp < 12) {
-    regs_fewer<BITS == 16 ? 72 : 40>();
+    regs_fewer<72>();
     if (warp == 8) {
       // -------------------------------------------------------------- issue of the matrix products
       // The whole warp walks the loops and one elected lane issues: descriptors then stay in uniform
@@ -847,32 +873,35 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   } else {
     // ---------------------------------------------------------------- codes -> 16-bit operand tiles
     if constexpr (BITS < 16) {
-      regs_fewer<72>();
+      regs_fewer<80>();
       constexpr int PPR = D / 16;  // 16-code pieces of a row
-      const int tid = threadIdx.x - 384;
+      // four warps turn keys, four values: while one group waits for its stores to be visible to the tensor
+      // core, the other works
+      const int tid = (threadIdx.x - 384) & 127, kv = (warp - 12) >> 2;
       const int col = tid % PPR, r0 = tid / PPR;
-      Ring<C::NST> ring;
-      Ring<C::NRAW> raw;
+      int at = kv;  // place in the ring of operand tiles: keys even, values odd
+      uint32_t ph = 0, rph = 0;
       JobReader reader(jobs, b);
       Job job;
       while (ok) {
         ok = reader.next(job);
         if (job.tiles < 0) break;
-        for (int jj = 0; jj < 2 * job.tiles; ++jj) {
-          const int rest = job.kend - job.key0 - (jj >> 1) * CH_KEYS;
-          if (!mbar_wait(&b.empty[ring.i], ring.ph ^ 1u, CH_WAIT)) {
+        for (int j = 0; j < job.tiles; ++j) {
+          const int rest = job.kend - job.key0 - j * CH_KEYS;
+          if (!mbar_wait(&b.empty[at], ph ^ 1u, CH_WAIT)) {
             ok = false;
             break;
           }
-          uint8_t* tile = smem + C::RING + ring.i * C::TILE;
+          uint8_t* tile = smem + C::RING + at * C::TILE;
           constexpr int STEP = 128 / PPR, N = CH_RAW / STEP;  // rows between pieces, pieces of a thread
           constexpr int WORDS = BITS / 2;                     // of a piece
           for (int hf = 0; hf < 2; ++hf) {
-            if (!mbar_wait(&b.rfull[raw.i], raw.ph, CH_WAIT)) {
+            const int rs = 2 * kv + hf;
+            if (!mbar_wait(&b.rfull[rs], rph, CH_WAIT)) {
               ok = false;
               break;
             }
-            const uint8_t* src = smem + C::ROFF + raw.i * C::RAW;
+            const uint8_t* src = smem + C::ROFF + rs * C::RAW;
             uint8_t* dst = tile + hf * CH_RAW * 128;
             const int left = rest - hf * CH_RAW;
             uint32_t wd[N][WORDS];
@@ -915,14 +944,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 0 : 1))) = o ? lo : hi;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b.rempty[raw.i]);
-            raw.step();
+            if (lane == 0) mbar_arrive(&b.rempty[rs]);
           }
           if (!ok) break;
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b.full[ring.i]);
-          ring.step();
+          if (lane == 0) mbar_arrive(&b.full[at]);
+          rph ^= 1u;
+          if ((at += 2) >= C::NST) {
+            at = kv;
+            ph ^= 1u;
+          }
         }
       }
     }
@@ -930,7 +962,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   if (!ok) atomicExch(&g_chunk_status, kStatusTimeout);
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) odd[blockIdx.x] = any_odd;
+  if (threadIdx.x == 0) odd[blockIdx.x] = *any_odd;
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -942,7 +974,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 constexpr int CJ_THREADS = CH_ROWS;
 template <typename T, int D>
 __global__ void __launch_bounds__(CJ_THREADS) chunk_join_kernel(const Args a, const Share sh, const float* __restrict__ part) {
-  __shared__ int64_t plan[3];
+  __shared__ int64_t plan[3 + CJ_THREADS / 32];
   Piece p;
   int64_t per;
   next_may_start();

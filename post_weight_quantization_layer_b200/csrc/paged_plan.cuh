@@ -29,10 +29,9 @@ __device__ __forceinline__ int units_of(const Args& a, const Share& sh, int unit
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
 
-// Inclusive sum over the block; every thread also gets the total.
+// Inclusive sum over the block; every thread also gets the total.  ws: THREADS / 32 words of shared memory.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total) {
-  __shared__ int64_t ws[THREADS / 32];
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total, int64_t* ws) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t x = shfl_up64(v, o);
@@ -57,6 +56,7 @@ __device__ __forceinline__ int64_t share_of(const Share& sh, int64_t line) {
 // Length of the line before sequence s, and the share; returns the units of s.  All threads.
 template <int THREADS>
 __device__ int64_t piece_line(const Args& a, const Share& sh, int unit, int s, int64_t& before, int64_t& per) {
+  __shared__ int64_t ws[THREADS / 32];
   int64_t all = 0, pre = 0, own = 0;
   for (int x = threadIdx.x; x < a.seqs; x += THREADS) {
     const int64_t u = units_of(a, sh, unit, x);
@@ -64,8 +64,8 @@ __device__ int64_t piece_line(const Args& a, const Share& sh, int unit, int s, i
     if (x < s) pre += u;
   }
   int64_t total;
-  block_scan<THREADS>(all, total);
-  block_scan<THREADS>(pre, before);
+  block_scan<THREADS>(all, total, ws);
+  block_scan<THREADS>(pre, before, ws);
   before *= a.kv_heads;
   per = share_of(sh, total * a.kv_heads);
   own = units_of(a, sh, unit, s);
@@ -86,6 +86,7 @@ __device__ __forceinline__ void set_whole(const Args& a, const Share& sh, int un
 // The first piece of this CTA's share; false if it has none.  All threads.
 template <int THREADS>
 __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c, Cursor* shared) {
+  __shared__ int64_t ws[THREADS / 32];
   if (sh.whole) {
     c.at = blockIdx.x;
     c.end = static_cast<int64_t>(a.seqs) * a.kv_heads;
@@ -94,7 +95,7 @@ __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c,
   }
   int64_t all = 0, total;
   for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += units_of(a, sh, unit, x);
-  block_scan<THREADS>(all, total);
+  block_scan<THREADS>(all, total, ws);
   total *= a.kv_heads;
   const int64_t per = share_of(sh, total);
   c.at = blockIdx.x * per;
@@ -105,7 +106,7 @@ __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c,
     const int x = x0 + threadIdx.x;
     const int64_t u = x < a.seqs ? static_cast<int64_t>(units_of(a, sh, unit, x)) * a.kv_heads : 0;
     int64_t sum;
-    const int64_t incl = block_scan<THREADS>(u, sum);
+    const int64_t incl = block_scan<THREADS>(u, sum, ws);
     const int64_t lo = base + incl - u;
     if (u && lo <= c.at && c.at < lo + u) {
       const int64_t per_head = u / a.kv_heads, rem = c.at - lo;
