@@ -164,12 +164,40 @@ int launch_next(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStre
   return after_launch();
 }
 
-// paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).
+// An item (the rows of a sequence and kv head, or a tile of them) that the border before share c cuts; told by
+// CTA c where no earlier border cuts the same item.  Its parts lie in the first slots of the CTAs c0 + 1 .. c1
+// and in slot `slot0` of c0 (a CTA's first piece is in its slot 0, its last in slot 1).
+struct Cut {
+  int c0, c1, slot0;  // c1 < 0: nothing to join
+  int start, n, head, tile;
+};
+
+// The cut at a CTA's first piece, which begins `skipped` units inside its item of `units`.
+__device__ __forceinline__ Cut cut_at(int64_t at, int64_t per, int skipped, int units, const Seq& q, int head, int tile) {
+  Cut c{0, -1, 0, q.start, q.n, head, tile};
+  if (skipped > 0) {
+    const int64_t begin = at - skipped;
+    c.c0 = static_cast<int>(begin / per);
+    c.slot0 = begin == c.c0 * per ? 0 : 1;
+    if (c.c0 + 1 == static_cast<int>(blockIdx.x)) c.c1 = static_cast<int>((begin + units - 1) / per);
+  }
+  return c;
+}
+
+// paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).  step_grid: CTAs, and whether
+// items can be cut; a part of a cut item is step_part(head_dim) floats.
 constexpr int kStepRows = 16;
-// `next`: follows a launch of the same call.
-int run_step(const Args& a, int dtype, int head_dim, int bits, bool next, cudaStream_t s);
-// paged_chunk.cu: the sequences with more rows.
-int run_chunk(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s);
+__host__ __device__ constexpr int step_part(int d) { return kStepRows * (d + 2); }
+int step_grid(const Args& a, bool* cuts);
+int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s);
+
+// paged_chunk.cu: the sequences with more rows, in tiles of kTileRows.  odd: a word per CTA, not 0 where it met
+// a result that is not finite.  `next`: follows a launch of the same call.
+constexpr int kTileRows = 256;
+__host__ __device__ constexpr int chunk_part(int d) { return kTileRows * (d + 2); }
+int run_chunk(const Args& a, int dtype, int head_dim, int bits, int grid, float* part, Cut* cut, int* odd, bool next,
+              cudaStream_t s);
+int run_chunk_redo(const Args& a, int dtype, int head_dim, int bits, const int* odd, int n, cudaStream_t s);
 int chunk_device_status(int clear);
 
 }  // namespace paged

@@ -35,7 +35,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int CH_ROWS = 256;  // rows of a tile
+constexpr int CH_ROWS = kTileRows;
 constexpr int CH_KEYS = 128;  // keys of a unit
 constexpr int CH_RAW = 64;    // keys of a staging slot
 constexpr uint32_t CH_WAIT = 1u << 22;
@@ -59,7 +59,9 @@ struct Cfg {
   static constexpr int BARS = ROFF + NRAW * RAW;
   static constexpr int NBARS = 2 * NST + 2 * NRAW + 16;
   static constexpr int JOBS = BARS + NBARS * 8 + 8;
-  static constexpr int SMEM = JOBS + 2 * 40 + 1024;
+  // 16-bit caches leave room to turn results round: 32 rows of 64 columns per softmax warp
+  static constexpr int OUT = (JOBS + 2 * 40 + 15) / 16 * 16;
+  static constexpr int SMEM = (BITS == 16 ? OUT + 8 * 4096 : JOBS + 2 * 40) + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -431,9 +433,9 @@ struct Ring {
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Args a,
-                 const Share sh, float* __restrict__ part, int* __restrict__ odd) {
+                 const Share sh, float* __restrict__ part, Cut* __restrict__ cut, int* __restrict__ odd) {
   using C = Cfg<D, BITS>;
-  constexpr int SIZE = (D + 2) * CH_ROWS;  // floats of a piece left behind
+  constexpr int SIZE = chunk_part(D);
   constexpr int KEEP = BITS == 16 ? 4 : 1;
   constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0u : 1u;
   extern __shared__ uint8_t smem_raw[];
@@ -443,8 +445,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   int64_t per;
   next_may_start();
   // (the operand ring is not in use yet)
-  if (!chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem))) {
-    if (threadIdx.x == 0) odd[blockIdx.x] = 0;
+  const bool any = chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem));
+  if (threadIdx.x == 0) {
+    cut[blockIdx.x] = any ? cut_at(p.at, per, p.u0, p.units, p.q, p.head, p.tile) : Cut{0, -1};
+    if (!any) odd[blockIdx.x] = 0;
+  }
+  if (!any) {
+    wait_for_last();
     return;
   }
   const int64_t first = p.at;
@@ -640,10 +647,32 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         if (mine) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) mine[(c * 32 + e) * CH_ROWS] = o[e];
-        } else if (in) {
-          uint32_t v[16];
+          continue;
+        }
+        uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
+        for (int e = 0; e < 16; ++e) v[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
+        if constexpr (BITS == 16) {
+          // through shared memory, so that 8 lanes store the 128 bytes of a row: a row per lane would touch 32
+          // lines with every store
+          uint8_t* turn = smem + C::OUT + warp * 4096;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(turn + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          if (c & 1) {
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = e * 4 + (lane >> 3);
+              T* to = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(in ? dst : nullptr), r));
+              if (to)
+                *reinterpret_cast<uint4*>(to + (c - 1) * 32 + (lane & 7) * 8) =
+                    *reinterpret_cast<const uint4*>(turn + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            }
+            __syncwarp();
+          }
+        } else if (in) {
           // a row per lane: the wider the stores, the fewer lines they touch
           if (wide) {
             store32(dst + c * 32, v);
@@ -967,53 +996,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-// Joins the pieces of every tile that was cut: CTA c takes the tile that the border between shares c and
-// c + 1 cuts, unless an earlier border cuts it too.
-constexpr int CJ_THREADS = CH_ROWS;
-template <typename T, int D>
-__global__ void __launch_bounds__(CJ_THREADS) chunk_join_kernel(const Args a, const Share sh, const float* __restrict__ part) {
-  __shared__ int64_t plan[3 + CJ_THREADS / 32];
-  Piece p;
-  int64_t per;
-  next_may_start();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) + 1;
-  const bool any = chunk_first<CJ_THREADS>(a, sh, c, p, per, plan);
   wait_for_last();
-  if (!any || p.u0 == 0) return;
-  const int64_t start = p.at - p.u0, end = start + p.units;
-  if ((c - 1) * per > start) return;
-  const int64_t c0 = c - 1, c1 = (end - 1) / per;
-  constexpr int64_t SIZE = (D + 2) * CH_ROWS;
-  const int rows = min(CH_ROWS, p.q.n * a.group - p.tile * CH_ROWS);
-  // 8 columns per CTA of the second grid dimension, a row per thread
-  const int r = threadIdx.x, col = blockIdx.y * 8;
-  if (r < rows) {
-    float m = -INFINITY, l = 0.f, v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    for (int64_t x = c0; x <= c1; ++x) {
-      const float* q = part + (2 * x + (x == c0 && start != c0 * per ? 1 : 0)) * SIZE;
-      const float pm = q[D * CH_ROWS + r], pl = q[(D + 1) * CH_ROWS + r];
-      const float mm = fmaxf(m, pm), ref = mm == -INFINITY ? 0.f : mm;
-      const float f0 = ex2(m - ref), f1 = ex2(pm - ref);
-      m = mm;
-      l = l * f0 + pl * f1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] * f0 + q[(col + i) * CH_ROWS + r] * f1;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int row = p.tile * CH_ROWS + r, i = row / a.group;
-    T* dst = static_cast<T*>(a.out) +
-             ((static_cast<int64_t>(p.q.start) + i) * a.heads + p.head * a.group + (row - i * a.group)) * D + col;
-    uint4 w;
-    w.x = pack2<T>(v[0] * inv, v[1] * inv);
-    w.y = pack2<T>(v[2] * inv, v[3] * inv);
-    w.z = pack2<T>(v[4] * inv, v[5] * inv);
-    w.w = pack2<T>(v[6] * inv, v[7] * inv);
-    *reinterpret_cast<uint4*>(dst) = w;
-  }
 }
 
 // Where a CTA met an accumulator that is not finite, rows are looked at again: a value that a row does not
@@ -1088,7 +1071,7 @@ int cache_map(CUtensorMap* m, const void* base, const Args& a, int d) {
 }
 
 template <typename T, int D, int BITS>
-int run(const Args& a, cudaStream_t s) {
+int run(const Args& a, int grid, float* part, Cut* cut, int* odd, bool next, cudaStream_t s) {
   using C = Cfg<D, BITS>;
   GPTQ_TRY(ensure_smem_limit(reinterpret_cast<const void*>(chunk_kernel<T, D, BITS>), C::SMEM));
   CUtensorMap tk = {}, tv = {};
@@ -1101,26 +1084,27 @@ int run(const Args& a, cudaStream_t s) {
   sh.min_per = 8;
   sh.rows_lo = kStepRows + 1;
   sh.rows_hi = 0x7fffffff;
-  sh.grid = num_sms();
-  void* part = nullptr;
-  const size_t pieces = static_cast<size_t>(sh.grid) * 2 * (D + 2) * CH_ROWS * sizeof(float);
-  GPTQ_TRY(pool_alloc(&part, pieces + sh.grid * sizeof(int), s));
-  int* odd = reinterpret_cast<int*>(static_cast<char*>(part) + pieces);
-  chunk_kernel<T, D, BITS><<<sh.grid, C::THREADS, C::SMEM, s>>>(tk, tv, a, sh, static_cast<float*>(part), odd);
-  int st = after_launch();
-  if (st == GPTQ_OK && sh.grid > 1)
-    st = launch_next(chunk_join_kernel<T, D>, dim3(sh.grid - 1, D / 8), CJ_THREADS, 0, s, a, sh,
-                     static_cast<const float*>(part));
-  if (st == GPTQ_OK)
-    st = launch_next(chunk_redo_kernel<T, D, BITS>, dim3(sh.grid), 128, 0, s, a, static_cast<const int*>(odd), sh.grid);
-  pool_free(part, s);
-  return st;
+  sh.grid = grid;
+  if (next) return launch_next(chunk_kernel<T, D, BITS>, dim3(grid), C::THREADS, C::SMEM, s, tk, tv, a, sh, part, cut, odd);
+  chunk_kernel<T, D, BITS><<<grid, C::THREADS, C::SMEM, s>>>(tk, tv, a, sh, part, cut, odd);
+  return after_launch();
+}
+
+template <typename T, int D>
+int redo(const Args& a, int bits, const int* odd, int n, cudaStream_t s) {
+  if (bits == 16) return launch_next(chunk_redo_kernel<T, D, 16>, dim3(n), 128, 0, s, a, odd, n);
+  if (bits == 8) return launch_next(chunk_redo_kernel<T, D, 8>, dim3(n), 128, 0, s, a, odd, n);
+  return launch_next(chunk_redo_kernel<T, D, 4>, dim3(n), 128, 0, s, a, odd, n);
 }
 
 }  // namespace
 
-int run_chunk(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s) {
-#define GPTQ_CHUNK(T, D) return bits == 16 ? run<T, D, 16>(a, s) : bits == 8 ? run<T, D, 8>(a, s) : run<T, D, 4>(a, s)
+int run_chunk(const Args& a, int dtype, int head_dim, int bits, int grid, float* part, Cut* cut, int* odd, bool next,
+              cudaStream_t s) {
+#define GPTQ_CHUNK(T, D)                                                                                       \
+  return bits == 16  ? run<T, D, 16>(a, grid, part, cut, odd, next, s)                                          \
+         : bits == 8 ? run<T, D, 8>(a, grid, part, cut, odd, next, s)                                           \
+                     : run<T, D, 4>(a, grid, part, cut, odd, next, s)
   if (dtype == GPTQ_BF16) {
     if (head_dim == 128) GPTQ_CHUNK(__nv_bfloat16, 128);
     GPTQ_CHUNK(__nv_bfloat16, 64);
@@ -1128,6 +1112,12 @@ int run_chunk(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s) 
   if (head_dim == 128) GPTQ_CHUNK(__half, 128);
   GPTQ_CHUNK(__half, 64);
 #undef GPTQ_CHUNK
+}
+
+int run_chunk_redo(const Args& a, int dtype, int head_dim, int bits, const int* odd, int n, cudaStream_t s) {
+  if (dtype == GPTQ_BF16)
+    return head_dim == 128 ? redo<__nv_bfloat16, 128>(a, bits, odd, n, s) : redo<__nv_bfloat16, 64>(a, bits, odd, n, s);
+  return head_dim == 128 ? redo<__half, 128>(a, bits, odd, n, s) : redo<__half, 64>(a, bits, odd, n, s);
 }
 
 int chunk_device_status(int clear) {

@@ -17,6 +17,7 @@ struct Share {
 
 struct Cursor {
   int64_t at, end;  // position on the line (units; items where whole), and where the share ends
+  int64_t per;      // units of a share
   int s, head, u0, u1, units;
 };
 
@@ -53,25 +54,6 @@ __device__ __forceinline__ int64_t share_of(const Share& sh, int64_t line) {
   return max((line + sh.grid - 1) / sh.grid, static_cast<int64_t>(sh.min_per));
 }
 
-// Length of the line before sequence s, and the share; returns the units of s.  All threads.
-template <int THREADS>
-__device__ int64_t piece_line(const Args& a, const Share& sh, int unit, int s, int64_t& before, int64_t& per) {
-  __shared__ int64_t ws[THREADS / 32];
-  int64_t all = 0, pre = 0, own = 0;
-  for (int x = threadIdx.x; x < a.seqs; x += THREADS) {
-    const int64_t u = units_of(a, sh, unit, x);
-    all += u;
-    if (x < s) pre += u;
-  }
-  int64_t total;
-  block_scan<THREADS>(all, total, ws);
-  block_scan<THREADS>(pre, before, ws);
-  before *= a.kv_heads;
-  per = share_of(sh, total * a.kv_heads);
-  own = units_of(a, sh, unit, s);
-  return own;
-}
-
 __device__ __forceinline__ void set_whole(const Args& a, const Share& sh, int unit, Cursor& c) {
   for (; c.at < c.end; c.at += sh.grid) {
     c.s = static_cast<int>(c.at / a.kv_heads);
@@ -98,6 +80,7 @@ __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c,
   block_scan<THREADS>(all, total, ws);
   total *= a.kv_heads;
   const int64_t per = share_of(sh, total);
+  c.per = per;
   c.at = blockIdx.x * per;
   c.end = min(total, c.at + per);
   if (c.at >= c.end) return false;

@@ -142,7 +142,7 @@ __device__ __forceinline__ uint32_t sub_pair8(uint32_t w0, uint32_t w1, int b0, 
 }
 
 template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const Share sh, float* __restrict__ part) {
+__global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const Share sh, float* __restrict__ part, Cut* __restrict__ cut) {
   using Y = Lay<D, BITS>;
   using PT = typename std::conditional<BITS == 16, T, __nv_bfloat16>::type;  // type of P and V in their product
   constexpr int NT = Y::NT, NO = D / 8;
@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
   next_may_start();
 
   Cursor cur;
-  if (!first_piece<ST_THREADS>(a, sh, ST_UNIT, cur, &cur_s)) {
-    wait_for_last();
-    return;
-  }
+  const bool any = first_piece<ST_THREADS>(a, sh, ST_UNIT, cur, &cur_s);
+  if (cut && threadIdx.x == 0)
+    cut[blockIdx.x] = any ? cut_at(cur.at, cur.per, cur.u0, cur.units, sequence(a, cur.s), cur.head, 0) : Cut{0, -1};
+  if (!any) return;
   const int64_t first = cur.at;
   for (; cur.at < cur.end; next_piece(a, sh, ST_UNIT, cur)) {
     const Seq q = sequence(a, cur.s);
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
       }
     }
     const bool whole = cur.u0 == 0 && cur.u1 == cur.units;
-    float* mine = whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (cur.at == first ? 0 : 1)) * (16 * (D + 2));
+    float* mine = whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (cur.at == first ? 0 : 1)) * step_part(D);
     for (int e = threadIdx.x; e < rows * (D / 4); e += ST_THREADS) {
       const int row = e / (D / 4), c = (e % (D / 4)) * 4;
       float mm = -INFINITY;
@@ -463,95 +463,40 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
     }
     __syncthreads();
   }
-  wait_for_last();
 }
 
-// Joins the pieces of every (sequence, kv head) that was cut.
-template <typename T, int D>
-__global__ void __launch_bounds__(ST_THREADS) step_join_kernel(const Args a, const Share sh, const float* __restrict__ part) {
-  const int s = blockIdx.x, h = blockIdx.y;
-  const Seq q = sequence(a, s);
-  const int rows = q.n * a.group;
-  int64_t at, per;
-  next_may_start();
-  const int64_t units = piece_line<ST_THREADS>(a, sh, ST_UNIT, s, at, per);
-  wait_for_last();
-  if (units == 0) return;
-  at += h * units;
-  const int64_t c0 = at / per, c1 = (at + units - 1) / per;
-  if (c0 == c1) return;
-  constexpr int SZ = 16 * (D + 2);
-  for (int e = threadIdx.x; e < rows * (D / 4); e += ST_THREADS) {
-    const int row = e / (D / 4), c = (e % (D / 4)) * 4;
-    float m = -INFINITY, l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t x = c0; x <= c1; ++x) {
-      // a CTA's first piece lies in its slot 0, its last in slot 1
-      const float* p = part + (2 * x + (x == c0 && at != c0 * per ? 1 : 0)) * SZ;
-      const float pm = p[16 * D + row], pl = p[16 * D + 16 + row];
-      const float4 y = *reinterpret_cast<const float4*>(p + row * D + c);
-      const float mm = fmaxf(m, pm), ref = mm == -INFINITY ? 0.f : mm;
-      const float f0 = ex2(m - ref), f1 = ex2(pm - ref);
-      m = mm;
-      l = l * f0 + pl * f1;
-      v.x = v.x * f0 + y.x * f1;
-      v.y = v.y * f0 + y.y * f1;
-      v.z = v.z * f0 + y.z * f1;
-      v.w = v.w * f0 + y.w * f1;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int i = row / a.group;
-    T* dst = static_cast<T*>(a.out) +
-             ((static_cast<int64_t>(q.start) + i) * a.heads + h * a.group + (row - i * a.group)) * D + c;
-    uint2 w;
-    w.x = pack2<T>(v.x * inv, v.y * inv);
-    w.y = pack2<T>(v.z * inv, v.w * inv);
-    *reinterpret_cast<uint2*>(dst) = w;
-  }
-}
+// Contexts of a few units are not cut: a piece per CTA, nothing to join.
+constexpr int ST_WHOLE = 8;
 
 template <typename T, int D, int BITS>
-int run(const Args& a, bool next, cudaStream_t s) {
+int run(const Args& a, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s) {
   constexpr int smem = (4 * 16 * D + 2 * 4 * 16) * static_cast<int>(sizeof(float));
-  const void* kern = reinterpret_cast<const void*>(step_kernel<T, D, BITS>);
-  GPTQ_TRY(ensure_smem_limit(kern, smem));
-  const int64_t keys = a.table_width << a.page_shift;
-  const int64_t items = static_cast<int64_t>(a.seqs) * a.kv_heads;
-  const int64_t most = items * ((keys + ST_UNIT - 1) / ST_UNIT);
+  GPTQ_TRY(ensure_smem_limit(reinterpret_cast<const void*>(step_kernel<T, D, BITS>), smem));
   Share sh;
-  // Contexts of a few units are not cut: a piece per CTA, no second launch.
-  sh.whole = keys <= 8 * ST_UNIT;
+  sh.whole = !cuts;
   sh.min_per = 4;
   sh.rows_lo = 1;
   sh.rows_hi = kStepRows;
-  sh.grid = static_cast<int>(std::min<int64_t>(sh.whole ? items : most, sh.whole ? (1 << 20) : 2 * num_sms()));
-  float* part = nullptr;
-  if (!sh.whole) {
-    void* w = nullptr;
-    GPTQ_TRY(pool_alloc(&w, static_cast<size_t>(sh.grid) * 2 * 16 * (D + 2) * sizeof(float), s));
-    part = static_cast<float*>(w);
-  }
-  int st;
-  if (next) {
-    st = launch_next(step_kernel<T, D, BITS>, dim3(sh.grid), ST_THREADS, smem, s, a, sh, part);
-  } else {
-    step_kernel<T, D, BITS><<<sh.grid, ST_THREADS, smem, s>>>(a, sh, part);
-    st = after_launch();
-  }
-  if (!sh.whole) {
-    if (st == GPTQ_OK)
-      st = launch_next(step_join_kernel<T, D>, dim3(a.seqs, a.kv_heads), ST_THREADS, 0, s, a, sh,
-                       static_cast<const float*>(part));
-    pool_free(part, s);
-  }
-  return st;
+  sh.grid = grid;
+  step_kernel<T, D, BITS><<<grid, ST_THREADS, smem, s>>>(a, sh, part, cuts ? cut : nullptr);
+  return after_launch();
 }
 
 }  // namespace
 
-int run_step(const Args& a, int dtype, int head_dim, int bits, bool next, cudaStream_t s) {
-#define GPTQ_STEP(T, D)                                                                                    \
-  return bits == 16 ? run<T, D, 16>(a, next, s) : bits == 8 ? run<T, D, 8>(a, next, s) : run<T, D, 4>(a, next, s)
+int step_grid(const Args& a, bool* cuts) {
+  const int64_t units = ((a.table_width << a.page_shift) + ST_UNIT - 1) / ST_UNIT;
+  const int64_t items = static_cast<int64_t>(a.seqs) * a.kv_heads;
+  *cuts = units > ST_WHOLE;
+  return static_cast<int>(*cuts ? std::min<int64_t>(items * units, 2 * num_sms()) : std::min<int64_t>(items, 1 << 20));
+}
+
+int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, bool cuts, float* part, Cut* cut,
+             cudaStream_t s) {
+#define GPTQ_STEP(T, D)                                                                                        \
+  return bits == 16  ? run<T, D, 16>(a, grid, cuts, part, cut, s)                                               \
+         : bits == 8 ? run<T, D, 8>(a, grid, cuts, part, cut, s)                                                \
+                     : run<T, D, 4>(a, grid, cuts, part, cut, s)
   if (dtype == GPTQ_BF16) {
     if (head_dim == 128) GPTQ_STEP(__nv_bfloat16, 128);
     GPTQ_STEP(__nv_bfloat16, 64);
