@@ -8,7 +8,8 @@
 // other half.  512 columns of tensor memory: two S (128 each, P over them), two O (head_dim each).
 //
 //  * Roles: warps 0-3 and 4-7 softmax, rescaling and output of their half; warp 8 issues the matrix
-//    products; warp 9 brings keys and values; warps 12-19 (8- and 4-bit caches only) turn codes into
+//    products; warp 9 walks the CTA's share and brings keys and values; warps 10 and 11 bring the queries of a
+//    half; warps 12-19 (8- and 4-bit caches only) turn codes into
 //    16-bit operands.  Registers move from the last two to the first.
 //  * 16-bit pages come by TMA straight into the swizzled operand tiles.  Pages of codes come by bulk
 //    copies (codes, scales and zeros of a page and head are contiguous) into a staging ring, from
@@ -57,11 +58,9 @@ struct Cfg {
   static constexpr int RING = 2 * TILE;
   static constexpr int ROFF = RING + NST * TILE;
   static constexpr int BARS = ROFF + NRAW * RAW;
-  static constexpr int NBARS = 2 * NST + 2 * NRAW + 16;
+  static constexpr int NBARS = 2 * NST + 2 * NRAW + 18;
   static constexpr int JOBS = BARS + NBARS * 8 + 8;
-  // 16-bit caches leave room to turn results round: 32 rows of 64 columns per softmax warp
-  static constexpr int OUT = (JOBS + 2 * 40 + 15) / 16 * 16;
-  static constexpr int SMEM = (BITS == 16 ? OUT + 8 * 4096 : JOBS + 2 * 40) + 1024;
+  static constexpr int SMEM = JOBS + 2 * 40 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -111,26 +110,32 @@ template <int THREADS>
 __device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& p, int64_t& per, int64_t* shared) {
   int64_t all = 0, total;
   for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += head_units(a, x);
-  block_scan<THREADS>(all, total, shared + 3);
+  const int64_t upto = block_scan<THREADS>(all, total, shared + 3) * a.kv_heads;
   total *= a.kv_heads;
   per = share_of(sh, total);
   p.at = cta * per;
   p.end = min(total, p.at + per);
   if (p.at >= p.end) return false;
-  int64_t base = 0;
-  for (int x0 = 0; x0 < a.seqs; x0 += THREADS) {
-    const int x = x0 + threadIdx.x;
-    const int64_t u = x < a.seqs ? head_units(a, x) * a.kv_heads : 0;
-    int64_t sum;
-    const int64_t incl = block_scan<THREADS>(u, sum, shared + 3);
-    const int64_t lo = base + incl - u;
+  auto take = [&](int x, int64_t u, int64_t lo) {
     if (u && lo <= p.at && p.at < lo + u) {
       shared[0] = x;
       shared[1] = p.at - lo;
       shared[2] = u / a.kv_heads;
     }
-    base += sum;
-    if (base > p.at) break;
+  };
+  if (a.seqs <= THREADS) {
+    take(threadIdx.x, all * a.kv_heads, upto - all * a.kv_heads);
+  } else {
+    int64_t base = 0;
+    for (int x0 = 0; x0 < a.seqs; x0 += THREADS) {
+      const int x = x0 + threadIdx.x;
+      const int64_t u = x < a.seqs ? head_units(a, x) * a.kv_heads : 0;
+      int64_t sum;
+      const int64_t incl = block_scan<THREADS>(u, sum, shared + 3);
+      take(x, u, base + incl - u);
+      base += sum;
+      if (base > p.at) break;
+    }
   }
   __syncthreads();
   p.s = static_cast<int>(shared[0]);
@@ -378,7 +383,7 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 }
 
 struct Bars {
-  uint64_t *full, *empty, *rfull, *rempty, *jfull, *jempty, *qfull, *sfull, *pmost, *pfull, *odone, *zero, *done;
+  uint64_t *full, *empty, *rfull, *rempty, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull, *odone, *zero, *done;
 };
 
 // What the other warps have to know of a piece, as the warp that walks the line tells them through shared
@@ -388,8 +393,8 @@ struct Job {
   int head, tile;
   int key0, kend;     // keys of the piece
   int tiles;          // of CH_KEYS keys; -1: no piece is left
+  int tiles0;         // of which the first half's rows see some key
   int slot;           // where the part is left behind: 0 or 1 of the CTA; -1: the tile is whole
-  int pad;
 };
 static_assert(sizeof(Job) == 40, "Job");
 
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                  const Share sh, float* __restrict__ part, Cut* __restrict__ cut, int* __restrict__ odd) {
   using C = Cfg<D, BITS>;
   constexpr int SIZE = chunk_part(D);
-  constexpr int KEEP = BITS == 16 ? 4 : 1;
+  constexpr int KEEP = BITS == 16 ? 4 : 2;
   constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0u : 1u;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -465,7 +470,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   b.jfull = b.rempty + C::NRAW;
   b.jempty = b.jfull + 2;
   b.qfull = b.jempty + 2;
-  b.sfull = b.qfull + 2;
+  b.qfree = b.qfull + 2;
+  b.sfull = b.qfree + 2;
   b.pmost = b.sfull + 2;
   b.pfull = b.pmost + 2;
   b.odone = b.pfull + 2;
@@ -485,8 +491,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.jfull[i], 1);
-      mbar_init(&b.jempty[i], 9 + C::CONV / 32);  // softmax, issuing and converting warps
-      mbar_init(&b.qfull[i], 4);
+      mbar_init(&b.jempty[i], 11 + C::CONV / 32);  // softmax, issuing, query and converting warps
+      mbar_init(&b.qfull[i], 1);
+      mbar_init(&b.qfree[i], 1);
       mbar_init(&b.sfull[i], 1);
       mbar_init(&b.pmost[i], 4);
       mbar_init(&b.pfull[i], 4);
@@ -509,15 +516,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax, one thread per row
-    regs_more<BITS == 16 ? 216 : 120>();
+    regs_more<BITS == 16 ? 216 : 136>();
     const int w = warp >> 2, wr = (warp & 3) * 32 + lane;  // half, row of the half
     uint8_t* qs = smem + C::QOFF + w * C::TILE;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t S = tmem + lanes + w * 128, O = tmem + lanes + 256 + w * D;
     uint32_t sph = 0, oph = 0;
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
-    // a row of the tile, counted from the first token that the tile touches, is token r / group of it
-    const uint32_t recip = 65536u / a.group + 1u;  // r < 320: (r * recip) >> 16 is exact
     JobReader reader(jobs, b);
     Job job;
     auto next_job = [&]() {  // the next piece whose tile has this half
@@ -526,39 +531,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       } while (job.tiles >= 0 && job.tile * CH_ROWS + w * 128 >= job.n * a.group);
       return job.tiles >= 0;
     };
-    // Q of this half of the piece, 16 bytes a lane along the rows; rows past the last are zeros
-    auto load_q = [&]() {
-      const uint32_t row0 = job.tile * CH_ROWS, i0 = row0 / static_cast<uint32_t>(a.group), over = row0 - i0 * a.group;
-      const int rows = job.n * a.group - static_cast<int>(row0) - w * 128;
-      const T* base = static_cast<const T*>(a.q) + (job.start + i0) * a.q_ts + job.head * a.group * a.q_hs;
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
-        const int e = x * 128 + (threadIdx.x & 127), r = e / (D / 8), c = e % (D / 8);
-        const int rr = over + w * 128 + r, i = static_cast<int>((rr * recip) >> 16);
-        const T* src = base + (r < rows ? i * a.q_ts + (rr - i * a.group) * a.q_hs + c * 8 : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(qs + chunk_off(r, c))), "l"(src),
-                     "r"(r < rows ? 16 : 0)
-                     : "memory");
-      }
-    };
-    auto q_ready = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.qfull[w]);
-    };
-    bool more = next_job();
-    if (more) {
-      load_q();
-      q_ready();
-    }
-    while (more) {
+    while (next_job()) {
       const int row = job.tile * CH_ROWS + w * 128 + wr;
       const bool in = row < job.n * a.group;
-      const uint32_t row0 = job.tile * CH_ROWS, t0 = row0 / static_cast<uint32_t>(a.group);
-      const uint32_t rr = row - t0 * a.group, ti = (rr * recip) >> 16;
-      const int i = in ? t0 + ti : 0, h = job.head * a.group + (in ? rr - ti * a.group : 0);
-      const int tiles = job.tiles;
+      const int i = in ? static_cast<uint32_t>(row) / static_cast<uint32_t>(a.group) : 0;
+      const int h = job.head * a.group + (in ? row - i * a.group : 0);
+      const int tiles = w ? job.tiles : job.tiles0;
       int key = job.key0;
       const Seq q{job.start, job.n, job.len};
       const int see = in ? min(job.kend, seen(a, q, i)) : job.kend;  // rows past the last: what comes out is not used
@@ -612,17 +590,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         const float ref = m == -INFINITY ? 0.f : -m * a.scale_log2;
         l += weights<T, KEEP>(x, a.scale_log2, ref, S, key, see, least, &b.pmost[w], &b.pfull[w]);
-        if (j + 1 == tiles) {  // the last scores were there: Q's place is free for the next piece's
-          more = next_job();
-          if (more) load_q();
-        }
       }
       if (!ok) break;
-      if (!tiles) {
-        more = next_job();
-        if (more) load_q();
-      }
-      if (more) q_ready();
       if (tiles) {
         if (!mbar_wait(&b.odone[w], oph, CH_WAIT)) {
           ok = false;
@@ -652,27 +621,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
-        if constexpr (BITS == 16) {
-          // through shared memory, so that 8 lanes store the 128 bytes of a row: a row per lane would touch 32
-          // lines with every store
-          uint8_t* turn = smem + C::OUT + warp * 4096;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(turn + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)) =
-                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          if (c & 1) {
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = e * 4 + (lane >> 3);
-              T* to = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(in ? dst : nullptr), r));
-              if (to)
-                *reinterpret_cast<uint4*>(to + (c - 1) * 32 + (lane & 7) * 8) =
-                    *reinterpret_cast<const uint4*>(turn + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-            }
-            __syncwarp();
-          }
-        } else if (in) {
+        if (in) {
           // a row per lane: the wider the stores, the fewer lines they touch
           if (wide) {
             store32(dst + c * 32, v);
@@ -705,7 +654,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       uint32_t qph = 0, pph = 0;  // phases, a bit per half
       const uint32_t q0 = desc_lo(smem_u32(smem + C::QOFF), 16), k0 = desc_lo(smem_u32(smem + C::RING), 16);
       const uint32_t v0 = desc_lo(smem_u32(smem + C::RING), CH_KEYS * 128);
-      auto qk = [&](int w, int st) {
+      auto qk = [&](int w, int st, bool last) {
         const uint32_t qa = q0 + w * (C::TILE >> 4), kb = k0 + st * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -713,6 +662,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           umma_ss(tmem + w * 128, qa + off, kb + off, iqk, k > 0 ? 1u : 0u);
         }
         umma_commit(&b.sfull[w]);
+        if (last) umma_commit(&b.qfree[w]);  // the piece's last scores: its queries are done with
       };
       JobReader reader(jobs, b);
       Job job;
@@ -720,25 +670,22 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         ok = reader.next(job);
         if (job.tiles < 0) break;
         const bool two = job.n * a.group > job.tile * CH_ROWS + 128;  // the tile has a second half
-        const int tiles = job.tiles;
-        ok = mbar_wait(&b.qfull[0], qph & 1u, CH_WAIT);  // Q of this piece is in place
-        qph ^= 1u;
-        if (two) {
-          ok = ok && mbar_wait(&b.qfull[1], (qph >> 1) & 1u, CH_WAIT);
-          qph ^= 2u;
+        // tiles of each half: the second half's rows see at least as many keys
+        const int n0 = job.tiles0, n1 = two ? job.tiles : 0, tiles = max(n0, n1);
+        if (tiles) ok = mbar_wait(&b.full[ring.i], ring.ph, CH_WAIT);
+        if (!ok) break;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if ((w ? n1 : n0) == 0) continue;
+          ok = ok && mbar_wait(&b.qfull[w], (qph >> w) & 1u, CH_WAIT);  // Q of this piece is in place
+          qph ^= 1u << w;
+          tc_fence_after();
+          if (ok && lead) qk(w, ring.i, (w ? n1 : n0) == 1);
+          __syncwarp();
         }
         if (!ok) break;
         if (!tiles) continue;
-        if (!mbar_wait(&b.full[ring.i], ring.ph, CH_WAIT)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lead) {
-          qk(0, ring.i);
-          if (two) qk(1, ring.i);
-          umma_commit(&b.empty[ring.i]);
-        }
+        if (lead) umma_commit(&b.empty[ring.i]);
         __syncwarp();
         ring.step();
         for (int j = 0; j < tiles && ok; ++j) {
@@ -749,14 +696,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           const uint32_t kph = ring.ph;
           const bool more = j + 1 < tiles;
           if (more) ring.step();
+          ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
+          if (more) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (w == 1 && !two) break;
-            if (w == 0) {
-              ok = ok && mbar_wait(&b.full[vst], vph, CH_WAIT);
-              if (more) ok = ok && mbar_wait(&b.full[kst], kph, CH_WAIT);
-            }
-            const bool last = w == 1 || !two;  // half to use this tile of V, and of K
+            const int mine = w ? n1 : n0;
+            if (j >= mine) continue;
             const uint32_t vb = v0 + vst * (C::TILE >> 4);
             ok = ok && mbar_wait(&b.pmost[w], (pph >> w) & 1u, CH_WAIT);
             if (!ok) break;
@@ -775,13 +720,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 #pragma unroll
               for (int k = 6; k < CH_KEYS / 16; ++k)
                 umma_ts(tmem + 256 + w * D, tmem + w * 128 + k * 8, vb + k * (2048 >> 4), ipv, 1u);
-              if (last) umma_commit(&b.empty[vst]);
-              if (more) {
-                qk(w, kst);
-                if (last) umma_commit(&b.empty[kst]);
-              } else {
+              if (w == 1 || n1 <= j) umma_commit(&b.empty[vst]);  // no half after this one uses the values
+              if (j + 1 < mine)
+                qk(w, kst, j + 2 == mine);
+              else
                 umma_commit(&b.odone[w]);
-              }
+              if (more && (w == 1 || n1 <= j)) umma_commit(&b.empty[kst]);
             }
             __syncwarp();
           }
@@ -815,8 +759,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       for (; p.at < p.end && ok; chunk_next(a, p)) {
         const int tiles = p.kend > 0 ? p.u1 - p.u0 : 0;
         const bool whole = p.u0 == 0 && p.u1 == p.units;
-        ok = tell(Job{p.q.start, p.q.n, p.q.len, p.head, p.tile, p.u0 * CH_KEYS, min(p.u1 * CH_KEYS, p.kend), tiles,
-                      whole ? -1 : (p.at == first ? 0 : 1), 0});
+        const uint32_t mid = (static_cast<uint32_t>(p.tile) * CH_ROWS + 127) / static_cast<uint32_t>(a.group);
+        const int kend0 = seen(a, p.q, min(p.q.n - 1, static_cast<int>(mid)));
+        const int tiles0 = max(0, min(tiles, (kend0 + CH_KEYS - 1) / CH_KEYS - p.u0));
+        ok = tell(Job{p.q.start, p.q.n, p.q.len, p.head, p.tile, p.u0 * CH_KEYS, min(p.u1 * CH_KEYS, p.kend), tiles, tiles0,
+                      whole ? -1 : (p.at == first ? 0 : 1)});
         // a lane per box; the page of the next tile's box is looked up one tile ahead
         auto find = [&](int key) { return key + lane * box < p.kend && lane < boxes ? key_at(a, p.s, p.head, key + lane * box) : 0; };
         int64_t next = tiles ? find(p.u0 * CH_KEYS) : 0;
@@ -898,11 +845,52 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           mbar_wait(BITS == 16 ? &b.full[at] : &b.rfull[at], ph, CH_WAIT);
         }
       }
+    } else {
+      // -------------------------------------------------------------- queries of a half (warps 10, 11)
+      // 16 bytes a lane along the rows; rows past the last are zeros.  A half that sees no key of the piece takes
+      // no part in its products and has none brought.
+      const int w = warp - 10;
+      uint8_t* qs = smem + C::QOFF + w * C::TILE;
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a warp's copy
+      const int c = lane % LPR;
+      uint32_t ph = 1u;
+      JobReader reader(jobs, b);
+      Job job;
+      while (ok) {
+        ok = reader.next(job);
+        if (job.tiles < 0) break;
+        const int rows = job.n * a.group - job.tile * CH_ROWS - w * 128;
+        if (rows <= 0 || (w ? job.tiles : job.tiles0) == 0) continue;
+        if (!mbar_wait(&b.qfree[w], ph, CH_WAIT)) {
+          ok = false;
+          break;
+        }
+        ph ^= 1u;
+        const uint32_t row0 = job.tile * CH_ROWS + w * 128 + lane / LPR;
+        uint32_t i = row0 / static_cast<uint32_t>(a.group), g = row0 - i * a.group;  // token and head of the row
+        const T* base = static_cast<const T*>(a.q) + job.start * a.q_ts + job.head * a.group * a.q_hs + c * 8;
+#pragma unroll 4
+        for (int r = lane / LPR; r < 128; r += RPI) {
+          const T* src = r < rows ? base + i * a.q_ts + g * a.q_hs : base;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(qs + chunk_off(r, c))), "l"(src),
+                       "r"(r < rows ? 16 : 0)
+                       : "memory");
+          g += RPI;
+          while (g >= static_cast<uint32_t>(a.group)) {
+            g -= a.group;
+            ++i;
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.qfull[w]);
+      }
     }
   } else {
     // ---------------------------------------------------------------- codes -> 16-bit operand tiles
     if constexpr (BITS < 16) {
-      regs_fewer<80>();
+      regs_fewer<64>();
       constexpr int PPR = D / 16;  // 16-code pieces of a row
       // four warps turn keys, four values: while one group waits for its stores to be visible to the tensor
       // core, the other works

@@ -77,20 +77,14 @@ __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c,
   }
   int64_t all = 0, total;
   for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += units_of(a, sh, unit, x);
-  block_scan<THREADS>(all, total, ws);
+  const int64_t upto = block_scan<THREADS>(all, total, ws) * a.kv_heads;
   total *= a.kv_heads;
   const int64_t per = share_of(sh, total);
   c.per = per;
   c.at = blockIdx.x * per;
   c.end = min(total, c.at + per);
   if (c.at >= c.end) return false;
-  int64_t base = 0;
-  for (int x0 = 0; x0 < a.seqs; x0 += THREADS) {
-    const int x = x0 + threadIdx.x;
-    const int64_t u = x < a.seqs ? static_cast<int64_t>(units_of(a, sh, unit, x)) * a.kv_heads : 0;
-    int64_t sum;
-    const int64_t incl = block_scan<THREADS>(u, sum, ws);
-    const int64_t lo = base + incl - u;
+  auto take = [&](int x, int64_t u, int64_t lo) {
     if (u && lo <= c.at && c.at < lo + u) {
       const int64_t per_head = u / a.kv_heads, rem = c.at - lo;
       shared->s = x;
@@ -98,8 +92,20 @@ __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c,
       shared->head = static_cast<int>(rem / per_head);
       shared->u0 = static_cast<int>(rem % per_head);
     }
-    base += sum;
-    if (base > c.at) break;
+  };
+  if (a.seqs <= THREADS) {
+    take(threadIdx.x, all * a.kv_heads, upto - all * a.kv_heads);
+  } else {
+    int64_t base = 0;
+    for (int x0 = 0; x0 < a.seqs; x0 += THREADS) {
+      const int x = x0 + threadIdx.x;
+      const int64_t u = x < a.seqs ? static_cast<int64_t>(units_of(a, sh, unit, x)) * a.kv_heads : 0;
+      int64_t sum;
+      const int64_t incl = block_scan<THREADS>(u, sum, ws);
+      take(x, u, base + incl - u);
+      base += sum;
+      if (base > c.at) break;
+    }
   }
   __syncthreads();
   c.s = shared->s;
