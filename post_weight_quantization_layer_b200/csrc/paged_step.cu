@@ -41,22 +41,23 @@ constexpr int ST_THREADS = 128;  // 4 warps
 constexpr int ST_UNIT = 64;      // keys of a unit of the line
 
 // Words (32 bits) of a lane: of one key (a quarter of it) and of one value (an eighth).
-template <int D, int BITS>
+template <int D, int BITS, int NR>
 struct Lay {
   static constexpr int KW = D / 4 * BITS / 32;
   static constexpr int VW = D / 8 * BITS / 32;
   static constexpr int ROW = D * BITS / 8;                 // bytes of a vector
   static constexpr int CPR = ROW / 16;                     // 16-byte chunks of it
-  static constexpr int KPW = BITS == 16 ? 16 : 32;         // keys of a warp's step
-  static constexpr int NT = KPW / 8;                       // 8-key tiles of a step
+  static constexpr int KPW = BITS == 4 ? 32 : 16;          // keys of a warp's step
+  static constexpr int NK = KPW / 16;                      // 16-key groups of it
   static constexpr int KP = KW >= 4 ? 4 : KW;              // words of a contiguous piece
   static constexpr int VP = VW >= 4 ? 4 : VW;
   // a warp's ring in shared memory: keys, values, and for codes their scales and zeros, of a step per stage
   static constexpr int SIDE = BITS == 16 ? 0 : KPW * 10;
   static constexpr int STAGE = 2 * KPW * ROW + SIDE;
-  static constexpr int ROOM = 26624;                       // of a warp: 8 warps share an SM
+  static constexpr int CTAS = NR == 2 ? 2 : 3;            // of an SM
+  static constexpr int ROOM = CTAS == 2 ? 26624 : 17920;   // of a warp
   static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
-  static constexpr int PART = 16 * D * 4;                  // the warp's weighted sums afterwards
+  static constexpr int PART = 8 * NR * D * 4;              // the warp's weighted sums afterwards
   static constexpr int RING = STAGES * STAGE > PART ? STAGES * STAGE : PART;
   // Chunk c of row r lies at chunk c ^ key_turn(r) (value_turn(r)) of its row, so that the 8 lanes that a 16-byte
   // read serves at once (two keys, four pieces; four values, two pieces) touch all banks.
@@ -78,6 +79,12 @@ __device__ __forceinline__ void read_words(uint32_t at, uint32_t* w) {
 __device__ __forceinline__ uint32_t read_pair(uint32_t at) {  // two bytes
   uint16_t w;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at));
+  return w;
+}
+
+__device__ __forceinline__ uint32_t read_byte(uint32_t at) {
+  uint16_t w;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(w) : "r"(at));
   return w;
 }
 
@@ -142,16 +149,26 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 1024 + code of two codes as a pair of halves.
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) { return (w & 0x000f000fu) | 0x64006400u; }
+// Codes as pairs of halves: 1024 + code, or 1024 + 16 code of the upper nibbles of a byte, which come without
+// a shift; what meets them is divided by 16.
 __device__ __forceinline__ uint32_t low_bytes(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4140u); }
 __device__ __forceinline__ uint32_t high_bytes(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4342u); }
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t w) { return (w & 0x000f000fu) | 0x64006400u; }
+__device__ __forceinline__ uint32_t high_nibbles(uint32_t w) { return (w & 0x00f000f0u) | 0x64006400u; }
 
-template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const Share sh, float* __restrict__ part, Cut* __restrict__ cut) {
-  using Y = Lay<D, BITS>;
+// An 8 x 8 matrix of 16-bit values, a row of pairs per four lanes, turned round.
+__device__ __forceinline__ uint32_t turned(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
+
+template <typename T, int D, int BITS, int NR>
+__global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
+    step_kernel(const Args a, const Share sh, float* __restrict__ part, Cut* __restrict__ cut) {
+  using Y = Lay<D, BITS, NR>;
   using PT = typename std::conditional<BITS == 16, T, __half>::type;  // operands of the products
-  constexpr int NT = Y::NT, NO = D / 8;
+  constexpr int NK = Y::NK, NO = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];  // a ring per warp, then maxima and sums
   float* red_m = reinterpret_cast<float*>(smem + 4 * Y::RING);
   float* red_l = red_m + 4 * 16;
@@ -173,17 +190,18 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
     const int h = cur.head, s = cur.s;
     const int k0 = cur.u0 * ST_UNIT, k1 = min(cur.u1 * ST_UNIT, q.len);
     const T* qbase = static_cast<const T*>(a.q);
-    const bool two = rows > 8;  // rows g + 8 are in use
-    // keys seen by this lane's two rows; for codes: the row's power of two, and the sum of its query
-    int see[2];
-    float power[2] = {1.f, 1.f}, qsum[2] = {0.f, 0.f};
-    uint32_t qf[D / 16][4];
+    // The products have keys (or values' columns) as their 16 rows and 8 rows of the sequence as their columns:
+    // a lane holds the query of row g (of each 8) as an operand and the scores of rows 2t, 2t + 1.
+    uint32_t qf[NR][D / 16][2];
+    int see[NR][2], least = k1;
+    float power[NR][2], qsum[NR][2], qoff[NR][2];  // for codes: see below
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r;
+    for (int r = 0; r < NR; ++r) {
+      const int row = 8 * r + g;
       const bool in = row < rows;
       const int i = in ? row / a.group : 0;
-      see[r] = in ? min(k1, seen(a, q, i)) : 0;
+      const int mine = in ? min(k1, seen(a, q, i)) : 0;
+      least = min(least, in ? mine : k1);
       const T* qr = qbase + (q.start + i) * a.q_ts + (h * a.group + (in ? row - i * a.group : 0)) * a.q_hs;
       uint4 raw[D / 32];  // 8 elements: two contraction steps
 #pragma unroll
@@ -191,7 +209,9 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
         raw[kk] = make_uint4(0, 0, 0, 0);
         if (in) raw[kk] = __ldg(reinterpret_cast<const uint4*>(qr + key_elem<D, BITS>(t, kk)));
       }
+      float up = 1.f, sum = 0.f, base = 0.f;
       if constexpr (BITS < 16) {
+        // the row over a power of two, in float16, its sum, and what the codes' offsets make of it
         float top = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk)
@@ -201,60 +221,82 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = max(__float_as_int(top) >> 23, 1);  // biased exponent; infinity: NaN for the whole row
         const float down = ex < 255 ? __int_as_float((254 - ex) << 23) : __int_as_float(0x7fc00000);
-        power[r] = __int_as_float(ex << 23);
-        float sum = 0.f;
+        up = __int_as_float(ex << 23) * a.scale_log2;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
           __half2 w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const T* v = reinterpret_cast<const T*>(&raw[kk]) + 2 * e;
-            w[e] = __floats2half2_rn(to_f32(v[0]) * down, to_f32(v[1]) * down);
-            sum += __low2float(w[e]) + __high2float(w[e]);
+            // 4 bits: the codes of odd elements come 16 times as large
+            w[e] = __floats2half2_rn(to_f32(v[0]) * down, to_f32(v[1]) * (BITS == 4 ? down * 0.0625f : down));
+            const float x = __low2float(w[e]), y = __high2float(w[e]);
+            sum += x + (BITS == 4 ? 16.f * y : y);
+            base += x + y;
           }
           raw[kk] = *reinterpret_cast<const uint4*>(w);
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        qsum[r] = sum + __shfl_xor_sync(0xffffffffu, sum, 2);
-        power[r] *= a.scale_log2;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          base += __shfl_xor_sync(0xffffffffu, base, o);
+        }
       }
 #pragma unroll
       for (int kk = 0; kk < D / 32; ++kk) {
         const uint4 w = raw[kk];
         if constexpr (BITS == 4) {  // pairs (e, e + 4), as the codes' nibbles come out
-          qf[2 * kk][r] = __byte_perm(w.x, w.z, 0x5410);
-          qf[2 * kk][r + 2] = __byte_perm(w.x, w.z, 0x7632);
-          qf[2 * kk + 1][r] = __byte_perm(w.y, w.w, 0x5410);
-          qf[2 * kk + 1][r + 2] = __byte_perm(w.y, w.w, 0x7632);
+          qf[r][2 * kk][0] = __byte_perm(w.x, w.z, 0x5410);
+          qf[r][2 * kk][1] = __byte_perm(w.x, w.z, 0x7632);
+          qf[r][2 * kk + 1][0] = __byte_perm(w.y, w.w, 0x5410);
+          qf[r][2 * kk + 1][1] = __byte_perm(w.y, w.w, 0x7632);
         } else {
-          qf[2 * kk][r] = w.x;
-          qf[2 * kk][r + 2] = w.y;
-          qf[2 * kk + 1][r] = w.z;
-          qf[2 * kk + 1][r + 2] = w.w;
+          qf[r][2 * kk][0] = w.x;
+          qf[r][2 * kk][1] = w.y;
+          qf[r][2 * kk + 1][0] = w.z;
+          qf[r][2 * kk + 1][1] = w.w;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // from the lanes that hold rows 2t, 2t + 1
+        const int from = (2 * t + c) * 4;
+        see[r][c] = __shfl_sync(0xffffffffu, mine, from);
+        if constexpr (BITS < 16) {
+          power[r][c] = __shfl_sync(0xffffffffu, up, from);
+          qsum[r][c] = __shfl_sync(0xffffffffu, sum, from);
+          qoff[r][c] = 1024.f * __shfl_sync(0xffffffffu, base, from);
         }
       }
     }
-    float o[NO][4];
 #pragma unroll
-    for (int i = 0; i < NO; ++i)
+    for (int o = 4; o < 32; o <<= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    float o[NR][NO][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    // for codes: running maximum of the weights (base 2), which the weighted sum is held against, and what the
-    // codes' offsets add to it
-    float mw[2] = {-INFINITY, -INFINITY}, off[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
+    // Running maximum and sum.  For codes also the running maximum of the weights (base 2), which the weighted
+    // sum is held against, and what the codes' offsets add to it.
+    float m[NR][2], l[NR][2], mw[NR][2], off[NR][4];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      m[r][0] = m[r][1] = mw[r][0] = mw[r][1] = -INFINITY;
+      l[r][0] = l[r][1] = off[r][0] = off[r][1] = off[r][2] = off[r][3] = 0.f;
+    }
 
-    int64_t vecn[NT / 2];  // first vector of each 16 keys of the step to be loaded next
-    auto find = [&](int k, int64_t (&v)[NT / 2]) {
+    int64_t vecn[NK];  // first vector of each 16 keys of the step to be loaded next
+    auto find = [&](int k, int64_t (&v)[NK]) {
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j) v[j] = k + 16 * j < k1 ? key_at(a, s, h, k + 16 * j) : 0;
+      for (int j = 0; j < NK; ++j) v[j] = k + 16 * j < k1 ? key_at(a, s, h, k + 16 * j) : 0;
     };
     // a step's copies: the 16 keys of a group are contiguous in their page, 16 bytes a lane; what lies past the
     // piece is not loaded
     auto load = [&](int k, int stage) {
       const uint32_t at = ring + stage * Y::STAGE;
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j) {
+      for (int j = 0; j < NK; ++j) {
         if (k + 16 * j >= k1) continue;
         const uint8_t* ks = static_cast<const uint8_t*>(a.kc) + vecn[j] * Y::ROW + lane * 16;
         const uint8_t* vs = static_cast<const uint8_t*>(a.vc) + vecn[j] * Y::ROW + lane * 16;
@@ -298,123 +340,144 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
       asm volatile("cp.async.commit_group;" ::: "memory");
       const uint32_t at = ring + stage * Y::STAGE, side = at + 2 * Y::KPW * Y::ROW;
       if (++stage == Y::STAGES) stage = 0;
-      // ---- scores
-      float sc[NT][4];
+      // ---- scores, 16 keys at a time: a lane gets those of keys g, g + 8 and rows 2t, 2t + 1
+      float sc[NK][NR][4], lv[NK][2];  // scores (base 2), log2 of the values' scales
+      uint32_t vz[NK][2];              // values' zeros of keys 2t, 2t + 1 and 2t + 8, 2t + 9
+      float mx[NR][2], mwx[NR][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-        uint32_t kw[Y::KW];
+        for (int c = 0; c < 2; ++c) {
+          mx[r][c] = m[r][c];
+          mwx[r][c] = mw[r][c];
+        }
+      const bool all = k + Y::KPW <= least;  // every row sees every key of the step
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        uint32_t ka[Y::KW], kb[Y::KW];
 #pragma unroll
         for (int j = 0; j < Y::KW / Y::KP; ++j) {
           const int byte = (j * 4 + t) * Y::KP * 4;  // of the key's row
-          read_words<Y::KP>(at + (nt * 8 + g) * Y::ROW + (((byte >> 4) ^ Y::key_turn(g)) << 4) + (byte & 15), kw + j * Y::KP);
+          const uint32_t from = at + (kk * 16 + g) * Y::ROW + (((byte >> 4) ^ Y::key_turn(g)) << 4) + (byte & 15);
+          read_words<Y::KP>(from, ka + j * Y::KP);
+          read_words<Y::KP>(from + 8 * Y::ROW, kb + j * Y::KP);
         }
-        if constexpr (BITS == 16) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma<PT>(sc[nt], qf[ks], kw[2 * ks], kw[2 * ks + 1]);
-        } else {
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            if constexpr (BITS == 8) {
-              const uint32_t w = kw[ks];
-              mma<PT>(sc[nt], qf[ks], low_bytes(w), high_bytes(w));
-            } else {
-              const uint32_t w = kw[ks >> 1] >> ((ks & 1) * 8);
-              mma<PT>(sc[nt], qf[ks], nibbles(w), nibbles(w >> 4));
-            }
+          for (int e = 0; e < 4; ++e) sc[kk][r][e] = BITS < 16 ? -qoff[r][e & 1] : 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t f[4];
+          if constexpr (BITS == 16) {
+            f[0] = ka[2 * ks];
+            f[1] = kb[2 * ks];
+            f[2] = ka[2 * ks + 1];
+            f[3] = kb[2 * ks + 1];
+          } else if constexpr (BITS == 8) {
+            f[0] = low_bytes(ka[ks]);
+            f[1] = low_bytes(kb[ks]);
+            f[2] = high_bytes(ka[ks]);
+            f[3] = high_bytes(kb[ks]);
+          } else {
+            const uint32_t x = ka[ks >> 1] >> ((ks & 1) * 8), y = kb[ks >> 1] >> ((ks & 1) * 8);
+            f[0] = low_nibbles(x);
+            f[1] = low_nibbles(y);
+            f[2] = high_nibbles(x);
+            f[3] = high_nibbles(y);
+          }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) mma<PT>(sc[kk][r], f, qf[r][ks][0], qf[r][ks][1]);
+        }
+        float scale[2], zero[2];
+        if constexpr (BITS < 16) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = kk * 16 + 8 * x + g;
+            uint32_t w;
+            read_words<1>(side + 4 * key, &w);
+            scale[x] = __uint_as_float(w);
+            read_words<1>(side + 4 * (Y::KPW + key), &w);
+            lv[kk][x] = lg2(__uint_as_float(w));
+            zero[x] = __uint_as_float(0x4B000000u | read_byte(side + 8 * Y::KPW + key)) - 8388608.f;
+            vz[kk][x] = read_pair(side + 9 * Y::KPW + kk * 16 + 8 * x + 2 * t);
           }
         }
-      }
-      // ---- softmax: rows g and g + 8; a key that a row does not see weighs nothing, whatever it holds
-      float mx[2] = {m[0], m[1]}, mwx[2] = {mw[0], mw[1]};
-      float lv[NT][2];   // log2 of the values' scales
-      uint32_t vz[NT];  // their zeros, two bytes
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float zk[2], ks[2];
-        if constexpr (BITS < 16) {  // of keys 2t, 2t + 1 of the tile
-          uint32_t w[2];
-          read_words<2>(side + 4 * (nt * 8 + 2 * t), w);
-          ks[0] = __uint_as_float(w[0]);
-          ks[1] = __uint_as_float(w[1]);
-          read_words<2>(side + 4 * (Y::KPW + nt * 8 + 2 * t), w);
-          lv[nt][0] = lg2(__uint_as_float(w[0]));
-          lv[nt][1] = lg2(__uint_as_float(w[1]));
-          const uint32_t z = read_pair(side + 8 * Y::KPW + nt * 8 + 2 * t);
-          vz[nt] = read_pair(side + 9 * Y::KPW + nt * 8 + 2 * t);
-          zk[0] = __uint_as_float(0x4B000000u | (z & 255u)) - 8387584.f;  // 2^23 - 1024: 1024 + zero
-          zk[1] = __uint_as_float(0x4B000000u | (z >> 8)) - 8387584.f;
-        }
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (e >= 2 && !two) continue;
-          const int r = e >> 1, c = e & 1;
-          float x;
-          if constexpr (BITS < 16)
-            x = fmaf(-zk[c], qsum[r], sc[nt][e]) * (ks[c] * power[r]);
-          else
-            x = sc[nt][e] * a.scale_log2;
-          x = k + nt * 8 + 2 * t + c < see[r] ? x : -INFINITY;
-          sc[nt][e] = x;
-          mx[r] = fmaxf(mx[r], x);
-          if constexpr (BITS < 16) mwx[r] = fmaxf(mwx[r], x + lv[nt][c]);
-        }
+          for (int e = 0; e < 4; ++e) {
+            float x = sc[kk][r][e];
+            if constexpr (BITS < 16)
+              x = fmaf(-zero[e >> 1], qsum[r][e & 1], x) * (scale[e >> 1] * power[r][e & 1]);
+            else
+              x *= a.scale_log2;
+            // a key that a row does not see weighs nothing, whatever it holds
+            if (!all && k + kk * 16 + 8 * (e >> 1) + g >= see[r][e & 1]) x = -INFINITY;
+            sc[kk][r][e] = x;
+            mx[r][e & 1] = fmaxf(mx[r][e & 1], x);
+            if constexpr (BITS < 16) mwx[r][e & 1] = fmaxf(mwx[r][e & 1], x + lv[kk][e >> 1]);
+          }
       }
+      // ---- softmax
       bool grown = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (r && !two) continue;
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        grown = grown || mx[r] > m[r];
-        if constexpr (BITS < 16) {
-          mwx[r] = fmaxf(mwx[r], __shfl_xor_sync(0xffffffffu, mwx[r], 1));
-          mwx[r] = fmaxf(mwx[r], __shfl_xor_sync(0xffffffffu, mwx[r], 2));
-          grown = grown || mwx[r] > mw[r];
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx[r][c] = fmaxf(mx[r][c], __shfl_xor_sync(0xffffffffu, mx[r][c], x));
+          grown = grown || mx[r][c] > m[r][c];
+          if constexpr (BITS < 16) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mwx[r][c] = fmaxf(mwx[r][c], __shfl_xor_sync(0xffffffffu, mwx[r][c], x));
+            grown = grown || mwx[r][c] > mw[r][c];
+          }
         }
-      }
       if (__any_sync(0xffffffffu, grown)) {
-        float corr[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          corr[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - mx[r]);
-          l[r] *= corr[r];
-          m[r] = mx[r];
-          if constexpr (BITS < 16) {
-            corr[r] = mw[r] == -INFINITY ? 0.f : ex2(mw[r] - mwx[r]);
-            mw[r] = mwx[r];
-            off[2 * r] *= corr[r];
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float f = m[r][c] == -INFINITY ? 0.f : ex2(m[r][c] - mx[r][c]);
+            l[r][c] *= f;
+            m[r][c] = mx[r][c];
+            if constexpr (BITS < 16) {
+              f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - mwx[r][c]);
+              mw[r][c] = mwx[r][c];
+              off[r][c] *= f;
+              off[r][2 + c] *= f;
+            }
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+              o[r][i][c] *= f;
+              o[r][i][2 + c] *= f;
+            }
           }
-        }
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= corr[e >> 1];
       }
-      uint32_t pf[NT][2];  // [tile][row half]
+      uint32_t pf[NK][NR][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (e >= 2 && !two) continue;
-          const int r = e >> 1;
-          const bool sees = k + nt * 8 + 2 * t + (e & 1) < see[r];
-          p[e] = sees ? ex2(sc[nt][e] - m[r]) : 0.f;
-          l[r] += p[e];
-          if constexpr (BITS < 16) {
-            const float ref = mw[r] == -INFINITY ? 0.f : mw[r];  // scales of zero alone so far
-            p[e] = sees ? ex2(sc[nt][e] + lv[nt][e & 1] - ref) : 0.f;
+        for (int r = 0; r < NR; ++r) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = e & 1;
+            const bool sees = all || k + kk * 16 + 8 * (e >> 1) + g < see[r][c];
+            p[e] = sees ? ex2(sc[kk][r][e] - m[r][c]) : 0.f;
+            l[r][c] += p[e];
+            if constexpr (BITS < 16) {
+              const float ref = mw[r][c] == -INFINITY ? 0.f : mw[r][c];  // scales of zero alone so far
+              p[e] = sees ? ex2(sc[kk][r][e] + lv[kk][e >> 1] - ref) : 0.f;
+            }
           }
+          pf[kk][r][0] = turned(pack2<PT>(p[0], p[1]));
+          pf[kk][r][1] = turned(pack2<PT>(p[2], p[3]));
         }
-        pf[nt][0] = pack2<PT>(p[0], p[1]);
-        pf[nt][1] = pack2<PT>(p[2], p[3]);
-      }
-      // ---- weighted sum
+      // ---- weighted sum: columns of the values (two of a lane's) by 16 keys
 #pragma unroll
-      for (int kk = 0; kk < NT / 2; ++kk) {
-        const uint32_t pa[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
+      for (int kk = 0; kk < NK; ++kk) {
         uint32_t vw[2][2][Y::VW];  // [8-key tile][key 2t, 2t + 1]
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -423,44 +486,46 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
 #pragma unroll
             for (int j = 0; j < Y::VW / Y::VP; ++j) {
               const int byte = (j * 8 + g) * Y::VP * 4;
-              read_words<Y::VP>(at + (Y::KPW + (2 * kk + x) * 8 + 2 * t + r) * Y::ROW +
+              read_words<Y::VP>(at + (Y::KPW + kk * 16 + x * 8 + 2 * t + r) * Y::ROW +
                                     (((byte >> 4) ^ Y::value_turn(2 * t + r)) << 4) + (byte & 15),
                                 vw[x][r] + j * Y::VP);
             }
             // a 16-bit value past the end of the keys must not meet its zero weight: it may be anything
-            if (BITS == 16 && k + Y::KPW > k1 && k + (2 * kk + x) * 8 + 2 * t + r >= k1) {
+            if (BITS == 16 && k + Y::KPW > k1 && k + kk * 16 + x * 8 + 2 * t + r >= k1) {
 #pragma unroll
               for (int e = 0; e < Y::VW; ++e) vw[x][r][e] = 0;
             }
           }
-        if constexpr (BITS == 16) {
+        if constexpr (BITS < 16) {  // the offsets' columns: 1024 + zero, and for 4 bits 1024
+          const uint32_t lo = low_bytes(vz[kk][0]), hi = low_bytes(vz[kk][1]);
+          const uint32_t f[4] = {lo, BITS == 4 ? 0x64006400u : lo, hi, BITS == 4 ? 0x64006400u : hi};
 #pragma unroll
-          for (int w = 0; w < Y::VW; ++w)
+          for (int r = 0; r < NR; ++r) mma<PT>(off[r], f, pf[kk][r][0], pf[kk][r][1]);
+        }
+        auto add = [&](int i, uint32_t f0, uint32_t f1, uint32_t f2, uint32_t f3) {
+          const uint32_t f[4] = {f0, f1, f2, f3};
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t sel = hf ? 0x7632u : 0x5410u;
-              mma<PT>(o[2 * w + hf], pa, __byte_perm(vw[0][0][w], vw[0][1][w], sel),
-                      __byte_perm(vw[1][0][w], vw[1][1][w], sel));
-            }
-        } else {
-          // the offsets' column: 1024 + zero of the four keys
-          mma<PT>(off, pa, low_bytes(vz[2 * kk]), low_bytes(vz[2 * kk + 1]));
+          for (int r = 0; r < NR; ++r) mma<PT>(o[r][i], f, pf[kk][r][0], pf[kk][r][1]);
+        };
 #pragma unroll
-          for (int w = 0; w < Y::VW; ++w) {
-            const uint32_t a0 = vw[0][0][w], a1 = vw[0][1][w];
-            const uint32_t b0 = vw[1][0][w], b1 = vw[1][1][w];
+        for (int w = 0; w < Y::VW; ++w) {
+          const uint32_t a0 = vw[0][0][w], a1 = vw[0][1][w], b0 = vw[1][0][w], b1 = vw[1][1][w];
+          if constexpr (BITS == 16) {
+            add(w, __byte_perm(a0, a1, 0x5410u), __byte_perm(a0, a1, 0x7632u), __byte_perm(b0, b1, 0x5410u),
+                __byte_perm(b0, b1, 0x7632u));
+          } else {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               if constexpr (BITS == 8) {
                 const uint32_t sel = hf ? 0x7362u : 0x5140u;  // bytes 2 hf, 2 hf + 1 of both keys
                 const uint32_t x = __byte_perm(a0, a1, sel), y = __byte_perm(b0, b1, sel);
-                mma<PT>(o[4 * w + 2 * hf], pa, low_bytes(x), low_bytes(y));
-                mma<PT>(o[4 * w + 2 * hf + 1], pa, high_bytes(x), high_bytes(y));
+                add(2 * w + hf, low_bytes(x), high_bytes(x), low_bytes(y), high_bytes(y));
               } else {
                 const uint32_t sel = hf ? 0x7632u : 0x5410u;
                 const uint32_t x = __byte_perm(a0, a1, sel), y = __byte_perm(b0, b1, sel);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) mma<PT>(o[8 * w + 4 * hf + b], pa, nibbles(x >> (4 * b)), nibbles(y >> (4 * b)));
+                add(4 * w + 2 * hf, low_nibbles(x), high_nibbles(x), low_nibbles(y), high_nibbles(y));
+                add(4 * w + 2 * hf + 1, low_nibbles(x >> 8), high_nibbles(x >> 8), low_nibbles(y >> 8),
+                    high_nibbles(y >> 8));
               }
             }
           }
@@ -470,30 +535,33 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     // ---- the four warps' parts, then the piece
-    if constexpr (BITS < 16) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float f = mw[r] == -INFINITY ? 0.f : ex2(mw[r] - m[r]);
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int i = 0; i < NO; ++i)
+      for (int c = 0; c < 2; ++c) {
+        const int row = 8 * r + 2 * t + c;
+        if constexpr (BITS < 16) {  // offsets off, and back to the row's own maximum
+          const float f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - m[r][c]);
+          const float off1 = BITS == 4 ? off[r][2 + c] + 16.f * (off[r][c] - off[r][2 + c]) : off[r][c];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) o[i][2 * r + c] = (o[i][2 * r + c] - off[2 * r]) * f;
+          for (int i = 0; i < NO; ++i) {
+            o[r][i][c] = (o[r][i][c] - off[r][c]) * f;
+            o[r][i][2 + c] = (o[r][i][2 + c] - off1) * (BITS == 4 ? f * 0.0625f : f);
+          }
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], x);
+        if (g == 0) {
+          red_m[warp * 16 + row] = m[r][c];
+          red_l[warp * 16 + row] = l[r][c];
+        }
+        if (row < rows) {
+#pragma unroll
+          for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) red(warp, row)[value_elem<D, BITS>(g, 2 * i + x)] = o[r][i][2 * x + c];
+        }
       }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t == 0) {
-        red_m[warp * 16 + g + 8 * r] = m[r];
-        red_l[warp * 16 + g + 8 * r] = l[r];
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-          if (g + 8 * r < rows) red(warp, g + 8 * r)[value_elem<D, BITS>(2 * t + c, i)] = o[i][2 * r + c];
-    }
     __syncthreads();
     if constexpr (BITS == 16) {
       // Keys that some rows of the tile see and others do not: a value there that is not finite has met
@@ -560,22 +628,31 @@ __global__ void __launch_bounds__(ST_THREADS, 2) step_kernel(const Args a, const
   }
 }
 
+// No sequence of the call has more than 8 rows here: half the products and registers.
+bool eight(const Args& a) { return static_cast<int64_t>(a.max_q) * a.group <= 8; }
+
 // Contexts of a few units are not cut: a piece per CTA, nothing to join.
 constexpr int ST_WHOLE = 8;
 
-template <typename T, int D, int BITS>
+template <typename T, int D, int BITS, int NR>
 int run(const Args& a, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s) {
-  constexpr int smem = 4 * Lay<D, BITS>::RING + 2 * 4 * 16 * static_cast<int>(sizeof(float));
-  static_assert(2 * (smem + 1024 + 512) <= 233472, "two CTAs share an SM");
-  GPTQ_TRY(ensure_smem_limit(reinterpret_cast<const void*>(step_kernel<T, D, BITS>), smem));
+  using Y = Lay<D, BITS, NR>;
+  constexpr int smem = 4 * Y::RING + 2 * 4 * 16 * static_cast<int>(sizeof(float));
+  static_assert(Y::STAGES >= 2 && Y::CTAS * (smem + 1024 + 256) <= 233472, "the CTAs of an SM share its memory");
+  GPTQ_TRY(ensure_smem_limit(reinterpret_cast<const void*>(step_kernel<T, D, BITS, NR>), smem));
   Share sh;
   sh.whole = !cuts;
   sh.min_per = 4;
   sh.rows_lo = 1;
   sh.rows_hi = kStepRows;
   sh.grid = grid;
-  step_kernel<T, D, BITS><<<grid, ST_THREADS, smem, s>>>(a, sh, part, cuts ? cut : nullptr);
+  step_kernel<T, D, BITS, NR><<<grid, ST_THREADS, smem, s>>>(a, sh, part, cuts ? cut : nullptr);
   return after_launch();
+}
+
+template <typename T, int D, int BITS>
+int run(const Args& a, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s) {
+  return eight(a) ? run<T, D, BITS, 1>(a, grid, cuts, part, cut, s) : run<T, D, BITS, 2>(a, grid, cuts, part, cut, s);
 }
 
 }  // namespace
@@ -584,7 +661,7 @@ int step_grid(const Args& a, bool* cuts) {
   const int64_t units = ((a.table_width << a.page_shift) + ST_UNIT - 1) / ST_UNIT;
   const int64_t items = static_cast<int64_t>(a.seqs) * a.kv_heads;
   *cuts = units > ST_WHOLE;
-  return static_cast<int>(*cuts ? std::min<int64_t>(items * units, 2 * num_sms()) : std::min<int64_t>(items, 1 << 20));
+  return static_cast<int>(*cuts ? std::min<int64_t>(items * units, (eight(a) ? 3 : 2) * num_sms()) : std::min<int64_t>(items, 1 << 20));
 }
 
 int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, bool cuts, float* part, Cut* cut,
