@@ -19,10 +19,11 @@ import ctypes
 import torch
 
 from ._native import lib
-from .api import _DTYPE, _check, _need, _need_cuda, _stream
+from .api import _DTYPE, _check, _need, _need_cuda
 
 SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
-_PARTS = ("k", "v", "k_scales", "k_zeros", "v_scales", "v_zeros")
+_PARTS = ("k", "v", "cache k_scales", "cache k_zeros", "cache v_scales", "cache v_zeros")
+_SIDE = (torch.float32, torch.uint8, torch.float32, torch.uint8)
 
 
 def _on(stream):
@@ -42,20 +43,36 @@ def _heads(x, what, dtype=None):
     return x.shape, (st[0] if x.shape[0] > 1 else 0), (st[1] if x.shape[1] > 1 else 0)
 
 
-def _here(*ts):
+def _here(dev, *ts):
     """CUDA tensors of the current device (strided ones allowed)."""
-    dev = torch.cuda.current_device() if ts[0].is_cuda else None
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
         if t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors")
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
-def _cache(cache, bits, kv_heads, head_dim, dtype):
-    """Pointers of a cache's tensors after checking them, and (pages, page_size).  kv_heads and
-    dtype are checked where given; head_dim None takes the cache's own (kv_heads and head_dim are
-    returned)."""
+def _plain(dev, t, what, dtype, shape):
+    """A contiguous tensor of one dtype and shape on the current device: one look where it is, the reasons
+    where it is not (single-token calls are as long as their checks)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return
+    _need(t, what, (dtype,), shape)
+    _need_cuda(t)
+
+
+def _device():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _cache(cache, bits, kv_heads, head_dim, dtype, dev):
+    """Pointers of a cache's tensors after checking them, and (pages, page_size, kv_heads, head_dim).
+    kv_heads, head_dim and dtype (of 16 bits) are checked where given."""
     if bits not in (16, 8, 4):
         raise ValueError("bits must be 16, 8 or 4")
     try:
@@ -66,16 +83,20 @@ def _cache(cache, bits, kv_heads, head_dim, dtype):
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("cache k must be a [pages, kv_heads, page_size, row] tensor")
     pages, H, P, row = k.shape
-    D = row * 16 // bits if bits == 16 else row * 8 // bits
-    want = (dtype,) if dtype is not None else (torch.float16, torch.bfloat16)
-    _need(k, "cache k", want if bits == 16 else (torch.uint8,),
-          (pages, kv_heads or H, P, (head_dim or D) * bits // 8 if bits < 16 else head_dim or D))
-    _need(v, "cache v", (k.dtype,), (pages, H, P, row))
-    if bits < 16:
-        for t, name, dt in zip(side, _PARTS[2:], (torch.float32, torch.uint8, torch.float32, torch.uint8)):
-            _need(t, f"cache {name}", (dt,), (pages, H, P))
-    _need_cuda(k, v, *side)
-    return [k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in side), *([None] * (6 - 2 - len(side)))], pages, P, H, D
+    D = row if bits == 16 else row * 8 // bits
+    if bits == 16:
+        want = dtype if dtype is not None else (k.dtype if k.dtype is torch.float16 else torch.bfloat16)
+    else:
+        want = torch.uint8
+    heads, d = kv_heads or H, head_dim or D
+    _plain(dev, k, "cache k", want, (pages, heads, P, d if bits == 16 else d * bits // 8))
+    _plain(dev, v, "cache v", want, k.shape)
+    if bits == 16:
+        return (k.data_ptr(), v.data_ptr(), None, None, None, None), pages, P, H, D
+    vectors = (pages, H, P)
+    for t, name, dt in zip(side, _PARTS[2:], _SIDE):
+        _plain(dev, t, name, dt, vectors)
+    return (k.data_ptr(), v.data_ptr(), *[t.data_ptr() for t in side]), pages, P, H, D
 
 
 def new_cache(pages, kv_heads, head_dim, page_size=64, bits=16, dtype=torch.bfloat16, device=None):
@@ -127,16 +148,16 @@ def rotary(q, k, positions, inv_freq, attention_factor=1.0, interleaved=False, o
         (Tk, Hk, Dk), kt, kh = _heads(k, "k", q.dtype)
         if (Tk, Dk) != (T, D):
             raise ValueError("k must have q's tokens and head_dim")
-    _need(positions, "positions", (torch.int32,), (T,))
+    dev = _device()
+    _plain(dev, positions, "positions", torch.int32, (T,))
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a 1-D float64 tensor")
-    _need(inv_freq, "inv_freq", (torch.float64,), (inv_freq.shape[0],))
-    _need_cuda(positions, inv_freq)
+    _plain(dev, inv_freq, "inv_freq", torch.float64, inv_freq.shape)
     if out is None:
-        _here(q) if k is None else _here(q, k)
+        _here(dev, q) if k is None else _here(dev, q, k)
         with _on(stream):
-            qo = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
-            ko = None if k is None else torch.empty(T, Hk, D, dtype=q.dtype, device=q.device)
+            qo = q.new_empty((T, Hq, D))
+            ko = None if k is None else q.new_empty((T, Hk, D))
         qot, qoh, kot, koh = Hq * D, D, Hk * D, D
     else:
         if not isinstance(out, (tuple, list)) or len(out) != 2 or (out[1] is None) != (k is None):
@@ -150,11 +171,11 @@ def rotary(q, k, positions, inv_freq, attention_factor=1.0, interleaved=False, o
             shape, kot, koh = _heads(ko, "out k", q.dtype)
             if tuple(shape) != (T, Hk, D):
                 raise ValueError("out k must have k's shape")
-        _here(*(t for t in (q, k, qo, ko) if t is not None))
+        _here(dev, *(t for t in (q, k, qo, ko) if t is not None))
     st = lib().gptq_rotary(q.data_ptr(), None if k is None else k.data_ptr(), _DTYPE[q.dtype], T, Hq, Hk, D,
                            2 * inv_freq.shape[0], 1 if interleaved else 0, qt, qh, kt, kh, positions.data_ptr(),
                            inv_freq.data_ptr(), attention_factor, qo.data_ptr(),
-                           None if ko is None else ko.data_ptr(), qot, qoh, kot, koh, _stream(stream))
+                           None if ko is None else ko.data_ptr(), qot, qoh, kot, koh, _raw_stream(stream, dev))
     _check(st, "gptq_rotary")
     return qo, ko
 
@@ -167,12 +188,12 @@ def cache_write(k, v, cache, slots, bits=16, stream=None):
     shape, vt, vh = _heads(v, "v", k.dtype)
     if tuple(shape) != (T, H, D):
         raise ValueError("v must have k's shape")
-    _need(slots, "slots", (torch.int32,), (T,))
-    ptrs, pages, P, _, _ = _cache(cache, bits, H, D, k.dtype)
-    _need_cuda(slots)
-    _here(k, v)
+    dev = _device()
+    ptrs, pages, P, _, _ = _cache(cache, bits, H, D, k.dtype, dev)
+    _plain(dev, slots, "slots", torch.int32, (T,))
+    _here(dev, k, v)
     st = lib().gptq_cache_write(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], T, H, D, kt, kh, vt, vh, *ptrs, bits,
-                                pages, P, slots.data_ptr(), _stream(stream))
+                                pages, P, slots.data_ptr(), _raw_stream(stream, dev))
     _check(st, "gptq_cache_write")
     return cache
 
@@ -187,15 +208,15 @@ def cache_read(cache, slots, bits=16, dtype=None, stream=None):
         raise ValueError("dtype must be float16 or bfloat16")
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D int32 tensor")
-    _need(slots, "slots", (torch.int32,), (slots.shape[0],))
-    ptrs, pages, P, H, D = _cache(cache, bits, None, None, dtype)
-    _need_cuda(slots)
+    dev = _device()
+    ptrs, pages, P, H, D = _cache(cache, bits, None, None, dtype, dev)
+    _plain(dev, slots, "slots", torch.int32, slots.shape)
     n = slots.shape[0]
     with _on(stream):
-        k = torch.empty(n, H, D, dtype=dtype, device=slots.device)
-        v = torch.empty(n, H, D, dtype=dtype, device=slots.device)
+        k = slots.new_empty((n, H, D), dtype=dtype)
+        v = slots.new_empty((n, H, D), dtype=dtype)
     st = lib().gptq_cache_read(*ptrs, bits, pages, P, slots.data_ptr(), n, H, D, _DTYPE[dtype], k.data_ptr(),
-                               v.data_ptr(), _stream(stream))
+                               v.data_ptr(), _raw_stream(stream, dev))
     _check(st, "gptq_cache_read")
     return k, v
 
@@ -213,28 +234,27 @@ def paged_attention(q, cache, page_table, kv_lens, q_starts, bits=16, max_q_len=
     scale:      of the scores, default head_dim ** -0.5
     Rows that see no key are zeros; rows of no sequence are left as they were in `out`."""
     (T, Hq, D), qt, qh = _heads(q, "q")
-    ptrs, pages, P, H, _ = _cache(cache, bits, None, D, q.dtype)
+    dev = _device()
+    ptrs, pages, P, H, _ = _cache(cache, bits, None, D, q.dtype, dev)
     if Hq % H:
         raise ValueError("heads must be a multiple of the cache's kv_heads")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [seqs, width] int32 tensor")
     S, width = page_table.shape
-    _need(page_table, "page_table", (torch.int32,), (S, width))
-    _need(kv_lens, "kv_lens", (torch.int32,), (S,))
-    _need(q_starts, "q_starts", (torch.int32,), (S + 1,))
-    _need_cuda(page_table, kv_lens, q_starts)
-    _here(q)
+    _plain(dev, page_table, "page_table", torch.int32, page_table.shape)
+    _plain(dev, kv_lens, "kv_lens", torch.int32, (S,))
+    _plain(dev, q_starts, "q_starts", torch.int32, (S + 1,))
+    _here(dev, q)
     if out is None:
         with _on(stream):
-            out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+            out = q.new_empty((T, Hq, D))
     else:
-        _need(out, "out", (q.dtype,), (T, Hq, D))
-        _need_cuda(out)
+        _plain(dev, out, "out", q.dtype, (T, Hq, D))
     if max_q_len is not None and (not isinstance(max_q_len, int) or max_q_len < 0):
         raise ValueError("max_q_len must be a number of rows")
     st = lib().gptq_paged_attention(q.data_ptr(), _DTYPE[q.dtype], T, Hq, H, D, qt, qh, *ptrs, bits, pages, P,
                                     page_table.data_ptr(), width, kv_lens.data_ptr(), q_starts.data_ptr(), S,
                                     T if max_q_len is None else max_q_len, 1 if causal else 0,
-                                    D ** -0.5 if scale is None else scale, out.data_ptr(), _stream(stream))
+                                    D ** -0.5 if scale is None else scale, out.data_ptr(), _raw_stream(stream, dev))
     _check(st, "gptq_paged_attention")
     return out
