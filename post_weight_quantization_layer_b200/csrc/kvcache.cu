@@ -3,13 +3,16 @@
 // One vector (a token's key or value of one kv head, D = 64 or 128 values) is one group of the
 // library's uniform quantizer: scale = (hi - lo) / maxq over a range that holds 0, an integer
 // zero point, value = scale * (code - zero).  The code is the one nearest to the exact quotient
-// x / s (half to even): k = rint(x * (1/s)) is at most one off, and the remainder
-// x - k s, which one fused multiply-add gives exactly, settles it against s / 2.  So the codes
-// do not depend on how a division rounds.
+// x / s (half to even): k = rint(x * (1/s)) is at most one off, and only where x * (1/s) lies
+// within its error of a half; there the remainder x - k s, which one fused multiply-add gives
+// exactly, settles it against s / 2.  So the codes do not depend on how a division rounds.
 //
-// Both directions are bound by memory.  A vector is D/8 neighbouring threads with 8 values (16
-// bytes) each: its range is a shuffle over them, and the codes leave as 8 or 4 bytes per
-// thread.  Keys and values go in one launch.
+// Both directions are bound by memory as long as a value costs few instructions: rounding by
+// adding 1.5 2^23 (the code is then the low byte), the range by packed 16-bit maxima of (x, -x)
+// that carry NaN along, the exact step behind a test of all 8 values.  (With the exact step for
+// every value and 64-bit index divisions, 8192 x 32 vectors of 128 took 80 us to write in 4 bits and 80
+// to read.)  A vector is D/8 neighbouring threads with 8 values (16 bytes) each: its range is a
+// shuffle over them, and the codes leave as 8 or 4 bytes per thread.  Keys and values go in one launch.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,6 +31,7 @@ struct CacheArgs {
   uint8_t *kz, *vz;
   int64_t count, slots_total;
   int heads, page_shift;
+  uint32_t per, magic;  // vectors of a token (keys and values of all heads), 2^32 / per rounded down
   const int32_t* slots;
 };
 
@@ -48,6 +52,35 @@ __device__ __forceinline__ float rint_quotient(float x, float s, float inv) {
   return k;
 }
 
+constexpr float ROUND = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits of the sum
+
+// Largest of pairs, NaN where one is NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_pair<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+__device__ __forceinline__ uint32_t max_pair<__half>(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Token (or slot) of a vector, and its side and head.
+__device__ __forceinline__ uint32_t token_of(const CacheArgs& p, uint32_t vec, int& sh) {
+  uint32_t t = __umulhi(vec, p.magic), rem = vec - t * p.per;
+  if (rem >= p.per) {
+    ++t;
+    rem -= p.per;
+  }
+  sh = static_cast<int>(rem);
+  return t;
+}
+
 // Offset (in vectors) of slot s, head h in [pages, heads, page_size]; -1 outside the cache.
 __device__ __forceinline__ int64_t vector_at(const CacheArgs& p, int slot, int h) {
   if (slot < 0 || slot >= p.slots_total) return -1;
@@ -55,76 +88,72 @@ __device__ __forceinline__ int64_t vector_at(const CacheArgs& p, int slot, int h
   return ((page * p.heads + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
 }
 
+// One vector's codes, scale and zero point, stored at vector `at` (all LPV threads of it call; at < 0: none).
 template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs p) {
-  constexpr int LPV = D / 8;  // threads of a vector
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * KC_THREADS + threadIdx.x;
-  const int64_t vec = e / LPV;
-  const int l = static_cast<int>(e % LPV);
-  // (token, side, head): whole groups of LPV threads (which never cross a warp) leave together
-  const int64_t per = 2 * p.heads;
-  const int64_t t = vec / per;
-  const int sh = static_cast<int>(vec - t * per);
-  const bool isv = sh >= p.heads;
-  const int h = isv ? sh - p.heads : sh;
-  const int64_t at = t < p.count ? vector_at(p, __ldg(p.slots + t), h) : -1;
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (at >= 0)
-    raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(isv ? p.v : p.k) + t * (isv ? p.v_ts : p.k_ts) +
-                                          h * (isv ? p.v_hs : p.k_hs) + l * 8);
+__device__ __forceinline__ void store_vector(const CacheArgs& p, bool isv, int64_t at, int l, const uint4 raw) {
+  constexpr int LPV = D / 8;
   if constexpr (BITS == 16) {
     if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(isv ? p.vc : p.kc) + at * D + l * 8) = raw;
   } else {
     constexpr float MAXQ = static_cast<float>((1 << BITS) - 1);
-    float x[8];
-    const T* r = reinterpret_cast<const T*>(&raw);
-    float lo = 0.f, hi = 0.f, bad = 0.f;
+    // (largest, largest of the negatives) of the vector, at least 0
+    constexpr uint32_t FLIP = 0x80008000u;
+    const uint32_t top = max_pair<T>(max_pair<T>(raw.x, raw.y), max_pair<T>(raw.z, raw.w));
+    const uint32_t low = max_pair<T>(max_pair<T>(raw.x ^ FLIP, raw.y ^ FLIP), max_pair<T>(raw.z ^ FLIP, raw.w ^ FLIP));
+    uint32_t ends = max_pair<T>(max_pair<T>(__byte_perm(top, low, 0x5410u), __byte_perm(top, low, 0x7632u)), 0u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = to_f32(r[i]);
-      lo = fminf(lo, x[i]);
-      hi = fmaxf(hi, x[i]);
-      bad += x[i] * 0.f;  // NaN as soon as one value is NaN or infinite
-    }
-#pragma unroll
-    for (int o = LPV / 2; o; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      bad += __shfl_xor_sync(0xffffffffu, bad, o);
-    }
+    for (int o = LPV / 2; o; o >>= 1) ends = max_pair<T>(ends, __shfl_xor_sync(0xffffffffu, ends, o));
     if (at < 0) return;
+    float hi = to_f32(reinterpret_cast<const T*>(&ends)[0]), lo = -to_f32(reinterpret_cast<const T*>(&ends)[1]);
     if (lo == 0.f && hi == 0.f) {
       lo = -1.f;
       hi = 1.f;
     }
     float s = __fdiv_rn(hi - lo, MAXQ);
-    uint32_t code[8];
+    float code[8];
     uint32_t zero = 0;
-    if (bad == 0.f && s < INFINITY) {
+    if (s < INFINITY) {
       // tiny scales are brought up by a power of two (exactly), where 1/s is finite
       const float up = s < 0x1p-100f ? 0x1p64f : 1.f;
       const float su = s * up, inv = __fdiv_rn(1.f, su);
       const float z = fminf(fmaxf(rint_quotient(-lo * up, su, inv), 0.f), MAXQ);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        code[i] = static_cast<uint32_t>(fminf(fmaxf(rint_quotient(x[i] * up, su, inv) + z, 0.f), MAXQ));
       zero = static_cast<uint32_t>(z);
-    } else {
+      const T* r = reinterpret_cast<const T*>(&raw);
+      float far = up == 1.f ? 0.f : 1.f;  // from an integer
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = to_f32(r[i]) * inv;
+        const float k = (q + ROUND) - ROUND;
+        far = fmaxf(far, fabsf(q - k));
+        code[i] = k;
+      }
+      // |q| < 256 carries three roundings: 256 * 3 * 2^-24 < 2^-14
+      if (far > 0.5f - 0x1p-14f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code[i] = rint_quotient(to_f32(r[i]) * up, su, inv);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) code[i] = fminf(fmaxf(code[i] + z, 0.f), MAXQ);
+    } else {  // NaN, or over the range
       s = __int_as_float(0x7fc00000);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = 0;
+      for (int i = 0; i < 8; ++i) code[i] = 0.f;
     }
     uint8_t* row = static_cast<uint8_t*>(isv ? p.vc : p.kc) + at * (D * BITS / 8);
     if constexpr (BITS == 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(code[i] + 8388608.f);  // the code in the low byte
       uint2 w;
-      w.x = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-      w.y = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+      w.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
+      w.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040u), __byte_perm(c[6], c[7], 0x0040u), 0x5410u);
       *reinterpret_cast<uint2*>(row + l * 8) = w;
     } else {
-      uint32_t w = 0;
+      uint32_t c[4];  // two codes in the low byte
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w |= code[i] << (4 * i);
-      *reinterpret_cast<uint32_t*>(row + l * 4) = w;
+      for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(fmaf(code[2 * i + 1], 16.f, code[2 * i]) + 8388608.f);
+      *reinterpret_cast<uint32_t*>(row + l * 4) =
+          __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
     }
     if (l == 0) {
       (isv ? p.vs : p.ks)[at] = s;
@@ -133,64 +162,119 @@ __global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs
   }
 }
 
-template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs p) {
-  constexpr int LPV = D / 8;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * KC_THREADS + threadIdx.x;
-  const int64_t vec = e / LPV;
-  const int l = static_cast<int>(e % LPV);
-  const int64_t per = 2 * p.heads;
-  const int64_t t = vec / per;
-  if (t >= p.count) return;
-  const int sh = static_cast<int>(vec - t * per);
-  const bool isv = sh >= p.heads;
-  const int h = isv ? sh - p.heads : sh;
-  const int64_t at = vector_at(p, __ldg(p.slots + t), h);
-  alignas(16) T out[8];
-  if (at < 0) {
+// U vectors per thread, loads before anything that waits for them: a thread's two loads depend on one another
+// (slot, then vector), so that one vector per thread leaves the memory idle (8192 x 32 vectors of 128: 137 us
+// to write and read in 4 bits).  Few vectors: one per thread, for the shortest way through.
+template <typename T, int D, int BITS, int U>
+__global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs p) {
+  constexpr int LPV = D / 8;             // threads of a vector
+  constexpr int VPC = KC_THREADS / LPV;  // vectors of a CTA at a time
+  const int l = threadIdx.x % LPV;
+  int64_t at[U];
+  uint4 raw[U];
+  bool isv[U];
+  // (token, side, head): the LPV threads of a vector never cross a warp
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = kc16<T>(0.f);
-  } else if constexpr (BITS == 16) {
-    *reinterpret_cast<uint4*>(out) =
-        __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(isv ? p.vc : p.kc) + at * D + l * 8));
-  } else {
-    const uint8_t* row = static_cast<const uint8_t*>(isv ? p.vc : p.kc) + at * (D * BITS / 8);
-    const float s = __ldg((isv ? p.vs : p.ks) + at);
-    const int z = __ldg((isv ? p.vz : p.kz) + at);
-    uint32_t w[2];
-    if constexpr (BITS == 8)
-      *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(row + l * 8));
-    else
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + l * 4));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = static_cast<int>((w[i * BITS / 32] >> (i * BITS % 32)) & ((1u << BITS) - 1u));
-      out[i] = kc16<T>(s * static_cast<float>(c - z));
+  for (int u = 0; u < U; ++u) {
+    int sh;
+    const int64_t t = token_of(p, (blockIdx.x * U + u) * VPC + threadIdx.x / LPV, sh);
+    isv[u] = sh >= p.heads;
+    const int h = isv[u] ? sh - p.heads : sh;
+    at[u] = -1;
+    raw[u] = make_uint4(0, 0, 0, 0);
+    if (t < p.count) {
+      at[u] = vector_at(p, __ldg(p.slots + t), h);
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(isv[u] ? p.v : p.k) +
+                                                    t * (isv[u] ? p.v_ts : p.k_ts) + h * (isv[u] ? p.v_hs : p.k_hs) + l * 8));
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<T*>(isv ? p.vo : p.ko) + (t * p.heads + h) * D + l * 8) =
-      *reinterpret_cast<const uint4*>(out);
+#pragma unroll
+  for (int u = 0; u < U; ++u) store_vector<T, D, BITS>(p, isv[u], at[u], l, raw[u]);
+}
+
+template <typename T, int D, int BITS, int U>
+__global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs p) {
+  constexpr int LPV = D / 8;
+  constexpr int VPC = KC_THREADS / LPV;
+  constexpr int W = BITS / 4;  // words of a thread's 8 values
+  const int l = threadIdx.x % LPV;
+  int64_t to[U], at[U];
+  bool isv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    int sh;
+    const int64_t t = token_of(p, (blockIdx.x * U + u) * VPC + threadIdx.x / LPV, sh);
+    isv[u] = sh >= p.heads;
+    const int h = isv[u] ? sh - p.heads : sh;
+    to[u] = t < p.count ? t * p.heads + h : -1;
+    at[u] = t < p.count ? vector_at(p, __ldg(p.slots + t), h) : -1;
+  }
+  uint32_t w[U][W];
+  float scale[U], zero[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[u][i] = 0;
+    scale[u] = 0.f;  // outside the cache: zeros
+    zero[u] = 8388608.f;
+    if (at[u] < 0) continue;
+    const uint8_t* from = static_cast<const uint8_t*>(isv[u] ? p.vc : p.kc) + at[u] * (D * BITS / 8) + l * BITS;
+    if constexpr (W == 4) {
+      *reinterpret_cast<uint4*>(w[u]) = __ldg(reinterpret_cast<const uint4*>(from));
+    } else {
+      if constexpr (W == 2)
+        *reinterpret_cast<uint2*>(w[u]) = __ldg(reinterpret_cast<const uint2*>(from));
+      else
+        w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(from));
+      scale[u] = __ldg((isv[u] ? p.vs : p.ks) + at[u]);
+      zero[u] = __uint_as_float(0x4B000000u | __ldg((isv[u] ? p.vz : p.kz) + at[u]));  // 2^23 + zero
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (to[u] < 0) continue;
+    alignas(16) T out[8];
+    if constexpr (BITS == 16) {
+      *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(w[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t c = (w[u][i * BITS / 32] >> (i * BITS % 32)) & ((1u << BITS) - 1u);
+        out[i] = kc16<T>(scale[u] * (__uint_as_float(0x4B000000u | c) - zero[u]));  // the difference is exact
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(isv[u] ? p.vo : p.ko) + to[u] * D + l * 8) =
+        *reinterpret_cast<const uint4*>(out);
+  }
+}
+
+template <typename T, int D, int U>
+void launch_cache(const CacheArgs& a, int bits, bool write, cudaStream_t s) {
+  constexpr int VPC = U * (KC_THREADS / (D / 8));
+  const unsigned grid = static_cast<unsigned>((a.count * 2 * a.heads + VPC - 1) / VPC);
+  if (write) {
+    if (bits == 16)
+      cache_write_kernel<T, D, 16, U><<<grid, KC_THREADS, 0, s>>>(a);
+    else if (bits == 8)
+      cache_write_kernel<T, D, 8, U><<<grid, KC_THREADS, 0, s>>>(a);
+    else
+      cache_write_kernel<T, D, 4, U><<<grid, KC_THREADS, 0, s>>>(a);
+  } else {
+    if (bits == 16)
+      cache_read_kernel<T, D, 16, U><<<grid, KC_THREADS, 0, s>>>(a);
+    else if (bits == 8)
+      cache_read_kernel<T, D, 8, U><<<grid, KC_THREADS, 0, s>>>(a);
+    else
+      cache_read_kernel<T, D, 4, U><<<grid, KC_THREADS, 0, s>>>(a);
+  }
 }
 
 template <typename T, int D>
 void launch_cache(const CacheArgs& a, int bits, bool write, cudaStream_t s) {
-  const int64_t threads = a.count * 2 * a.heads * (D / 8);
-  const unsigned grid = static_cast<unsigned>((threads + KC_THREADS - 1) / KC_THREADS);
-  if (write) {
-    if (bits == 16)
-      cache_write_kernel<T, D, 16><<<grid, KC_THREADS, 0, s>>>(a);
-    else if (bits == 8)
-      cache_write_kernel<T, D, 8><<<grid, KC_THREADS, 0, s>>>(a);
-    else
-      cache_write_kernel<T, D, 4><<<grid, KC_THREADS, 0, s>>>(a);
-  } else {
-    if (bits == 16)
-      cache_read_kernel<T, D, 16><<<grid, KC_THREADS, 0, s>>>(a);
-    else if (bits == 8)
-      cache_read_kernel<T, D, 8><<<grid, KC_THREADS, 0, s>>>(a);
-    else
-      cache_read_kernel<T, D, 4><<<grid, KC_THREADS, 0, s>>>(a);
-  }
+  if (a.count * 2 * a.heads >= 16384)
+    launch_cache<T, D, 4>(a, bits, write, s);
+  else
+    launch_cache<T, D, 1>(a, bits, write, s);
 }
 
 int launch_cache(const CacheArgs& a, int dtype, int head_dim, int bits, bool write, cudaStream_t s) {
@@ -238,12 +322,13 @@ extern "C" int gptq_cache_write(const void* k, const void* v, int dtype, int64_t
                        head_dim, dtype));
   if (((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7) || !aligned16(k) || !aligned16(v))
     return GPTQ_ERR_UNSUPPORTED;
-  if (tokens * 2 * kv_heads * (head_dim / 8) / KC_THREADS >= 2147483647LL) return GPTQ_ERR_UNSUPPORTED;
+  if (tokens * 2 * kv_heads > (int64_t(1) << 31)) return GPTQ_ERR_UNSUPPORTED;
   if (tokens == 0) return GPTQ_OK;
   int shift = 0;
   while ((1 << shift) < page_size) ++shift;
   CacheArgs a{k, v, nullptr, nullptr, k_token_stride, k_head_stride, v_token_stride, v_head_stride, k_cache, v_cache,
-              k_scales, v_scales, k_zeros, v_zeros, tokens, pages * page_size, kv_heads, shift, slots};
+              k_scales, v_scales, k_zeros, v_zeros, tokens, pages * page_size, kv_heads, shift, 2u * kv_heads,
+              static_cast<uint32_t>((uint64_t(1) << 32) / (2u * kv_heads)), slots};
   return launch_cache(a, dtype, head_dim, bits, true, static_cast<cudaStream_t>(stream));
 }
 
@@ -255,12 +340,13 @@ extern "C" int gptq_cache_read(const void* k_cache, const void* v_cache, const f
   GPTQ_TRY(check_cache(k_cache, v_cache, k_scales, k_zeros, v_scales, v_zeros, bits, pages, page_size, kv_heads,
                        head_dim, dtype));
   if (!aligned16(k) || !aligned16(v)) return GPTQ_ERR_UNSUPPORTED;
-  if (count * 2 * kv_heads * (head_dim / 8) / KC_THREADS >= 2147483647LL) return GPTQ_ERR_UNSUPPORTED;
+  if (count * 2 * kv_heads > (int64_t(1) << 31)) return GPTQ_ERR_UNSUPPORTED;
   if (count == 0) return GPTQ_OK;
   int shift = 0;
   while ((1 << shift) < page_size) ++shift;
   CacheArgs a{nullptr, nullptr, k, v, 0, 0, 0, 0, const_cast<void*>(k_cache), const_cast<void*>(v_cache),
               const_cast<float*>(k_scales), const_cast<float*>(v_scales), const_cast<uint8_t*>(k_zeros),
-              const_cast<uint8_t*>(v_zeros), count, pages * page_size, kv_heads, shift, slots};
+              const_cast<uint8_t*>(v_zeros), count, pages * page_size, kv_heads, shift, 2u * kv_heads,
+              static_cast<uint32_t>((uint64_t(1) << 32) / (2u * kv_heads)), slots};
   return launch_cache(a, dtype, head_dim, bits, false, static_cast<cudaStream_t>(stream));
 }
