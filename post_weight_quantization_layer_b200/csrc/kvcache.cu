@@ -88,76 +88,136 @@ __device__ __forceinline__ int64_t vector_at(const CacheArgs& p, int slot, int h
   return ((page * p.heads + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
 }
 
-// One vector's codes, scale and zero point, stored at vector `at` (all LPV threads of it call; at < 0: none).
+// Packed fp32 pairs (the f32x2 arithmetic of sm_100).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The 8 values of a thread as pairs.
+__device__ __forceinline__ void widen(const uint4 raw, float2 (&x)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void widen(const uint4 raw, float2 (&x)[4], __half) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+}
+
+// Bytes added without carries between them.
+__device__ __forceinline__ uint32_t add_bytes(uint32_t a, uint32_t b) {
+  return ((a & 0x7f7f7f7fu) + (b & 0x7f7f7f7fu)) ^ ((a ^ b) & 0x80808080u);
+}
+
+// (largest, largest of the negatives) of a thread's values and 0, NaN where one is NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t ends_of(const uint4 raw) {
+  constexpr uint32_t FLIP = 0x80008000u;
+  const uint32_t top = max_pair<T>(max_pair<T>(raw.x, raw.y), max_pair<T>(raw.z, raw.w));
+  const uint32_t low = max_pair<T>(max_pair<T>(raw.x ^ FLIP, raw.y ^ FLIP), max_pair<T>(raw.z ^ FLIP, raw.w ^ FLIP));
+  return max_pair<T>(max_pair<T>(__byte_perm(top, low, 0x5410u), __byte_perm(top, low, 0x7632u)), 0u);
+}
+
+// Scale, its reciprocal and the zero point of a vector from its ends.  A vector with a NaN, an infinity or a range
+// over float32's: scale NaN.
+struct Params {
+  float s, inv, z;
+};
+template <typename T, int BITS>
+__device__ __forceinline__ Params params_of(uint32_t ends) {
+  constexpr float MAXQ = static_cast<float>((1 << BITS) - 1);
+  float hi = to_f32(reinterpret_cast<const T*>(&ends)[0]), lo = -to_f32(reinterpret_cast<const T*>(&ends)[1]);
+  if (lo == 0.f && hi == 0.f) {
+    lo = -1.f;
+    hi = 1.f;
+  }
+  Params p;
+  p.s = __fdiv_rn(hi - lo, MAXQ);
+  p.inv = 0.f;
+  p.z = 0.f;
+  if (p.s < INFINITY) {
+    const float up = p.s < 0x1p-100f ? 0x1p64f : 1.f;  // as in store_vector
+    p.inv = __fdiv_rn(1.f, p.s * up);
+    p.z = fminf(fmaxf(rint_quotient(-lo * up, p.s * up, p.inv), 0.f), MAXQ);
+  } else {
+    p.s = __int_as_float(0x7fc00000);
+  }
+  return p;
+}
+
+// One vector's codes, scale and zero point, stored at vector `at` (at < 0: none).
 template <typename T, int D, int BITS>
-__device__ __forceinline__ void store_vector(const CacheArgs& p, bool isv, int64_t at, int l, const uint4 raw) {
-  constexpr int LPV = D / 8;
+__device__ __forceinline__ void store_vector(const CacheArgs& p, bool isv, int64_t at, int l, const uint4 raw,
+                                             const Params q) {
+  if (at < 0) return;
+  uint8_t* row = static_cast<uint8_t*>(isv ? p.vc : p.kc) + at * (D * BITS / 8);
   if constexpr (BITS == 16) {
-    if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(isv ? p.vc : p.kc) + at * D + l * 8) = raw;
+    *reinterpret_cast<uint4*>(row + l * 16) = raw;
   } else {
     constexpr float MAXQ = static_cast<float>((1 << BITS) - 1);
-    // (largest, largest of the negatives) of the vector, at least 0
-    constexpr uint32_t FLIP = 0x80008000u;
-    const uint32_t top = max_pair<T>(max_pair<T>(raw.x, raw.y), max_pair<T>(raw.z, raw.w));
-    const uint32_t low = max_pair<T>(max_pair<T>(raw.x ^ FLIP, raw.y ^ FLIP), max_pair<T>(raw.z ^ FLIP, raw.w ^ FLIP));
-    uint32_t ends = max_pair<T>(max_pair<T>(__byte_perm(top, low, 0x5410u), __byte_perm(top, low, 0x7632u)), 0u);
-#pragma unroll
-    for (int o = LPV / 2; o; o >>= 1) ends = max_pair<T>(ends, __shfl_xor_sync(0xffffffffu, ends, o));
-    if (at < 0) return;
-    float hi = to_f32(reinterpret_cast<const T*>(&ends)[0]), lo = -to_f32(reinterpret_cast<const T*>(&ends)[1]);
-    if (lo == 0.f && hi == 0.f) {
-      lo = -1.f;
-      hi = 1.f;
-    }
-    float s = __fdiv_rn(hi - lo, MAXQ);
-    float code[8];
-    uint32_t zero = 0;
-    if (s < INFINITY) {
+    uint32_t c[2] = {0, 0};  // codes as bytes
+    if (q.s == q.s) {
       // tiny scales are brought up by a power of two (exactly), where 1/s is finite
-      const float up = s < 0x1p-100f ? 0x1p64f : 1.f;
-      const float su = s * up, inv = __fdiv_rn(1.f, su);
-      const float z = fminf(fmaxf(rint_quotient(-lo * up, su, inv), 0.f), MAXQ);
-      zero = static_cast<uint32_t>(z);
-      const T* r = reinterpret_cast<const T*>(&raw);
-      float far = up == 1.f ? 0.f : 1.f;  // from an integer
+      const float up = q.s < 0x1p-100f ? 0x1p64f : 1.f;
+      const float su = q.s * up;
+      float2 x[4], t[4];
+      widen(raw, x, T());
+      float far = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = to_f32(r[i]) * inv;
-        const float k = (q + ROUND) - ROUND;
-        far = fmaxf(far, fabsf(q - k));
-        code[i] = k;
+      for (int i = 0; i < 4; ++i) {
+        x[i] = mul2(x[i], both(up));
+        t[i] = fma2(x[i], both(q.inv), both(ROUND));
+        const float2 k = add2(t[i], both(-ROUND));
+        const float2 e = fma2(k, both(-su), x[i]);  // exact, as in rint_quotient
+        far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
       }
-      // |q| < 256 carries three roundings: 256 * 3 * 2^-24 < 2^-14
-      if (far > 0.5f - 0x1p-14f) {
+      if (!(far < 0.5f * su)) {  // a tie, or one off beside a half
 #pragma unroll
-        for (int i = 0; i < 8; ++i) code[i] = rint_quotient(to_f32(r[i]) * up, su, inv);
+        for (int i = 0; i < 4; ++i) {
+          t[i].x = rint_quotient(x[i].x, su, q.inv) + ROUND;
+          t[i].y = rint_quotient(x[i].y, su, q.inv) + ROUND;
+        }
       }
+      // x >= lo leaves code >= 0 (rounding is odd); hi and zero may both round up
+      const float lim = ROUND + (MAXQ - q.z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = fminf(fmaxf(code[i] + z, 0.f), MAXQ);
-    } else {  // NaN, or over the range
-      s = __int_as_float(0x7fc00000);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = 0.f;
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __byte_perm(__float_as_uint(fminf(t[2 * i].x, lim)), __float_as_uint(fminf(t[2 * i].y, lim)), 0x0040u);
+        const uint32_t hi =
+            __byte_perm(__float_as_uint(fminf(t[2 * i + 1].x, lim)), __float_as_uint(fminf(t[2 * i + 1].y, lim)), 0x0040u);
+        c[i] = add_bytes(__byte_perm(lo, hi, 0x5410u), static_cast<uint32_t>(q.z) * 0x01010101u);
+      }
     }
-    uint8_t* row = static_cast<uint8_t*>(isv ? p.vc : p.kc) + at * (D * BITS / 8);
     if constexpr (BITS == 8) {
-      uint32_t c[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(code[i] + 8388608.f);  // the code in the low byte
-      uint2 w;
-      w.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
-      w.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040u), __byte_perm(c[6], c[7], 0x0040u), 0x5410u);
-      *reinterpret_cast<uint2*>(row + l * 8) = w;
+      *reinterpret_cast<uint2*>(row + l * 8) = make_uint2(c[0], c[1]);
     } else {
-      uint32_t c[4];  // two codes in the low byte
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(fmaf(code[2 * i + 1], 16.f, code[2 * i]) + 8388608.f);
-      *reinterpret_cast<uint32_t*>(row + l * 4) =
-          __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
+      // two codes to a byte
+      *reinterpret_cast<uint32_t*>(row + l * 4) = __byte_perm(c[0] | (c[0] >> 4), c[1] | (c[1] >> 4), 0x6420u);
     }
     if (l == 0) {
-      (isv ? p.vs : p.ks)[at] = s;
-      (isv ? p.vz : p.kz)[at] = static_cast<uint8_t>(zero);
+      (isv ? p.vs : p.ks)[at] = q.s;
+      (isv ? p.vz : p.kz)[at] = static_cast<uint8_t>(q.z);
     }
   }
 }
@@ -188,8 +248,27 @@ __global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs
                                                     t * (isv[u] ? p.v_ts : p.k_ts) + h * (isv[u] ? p.v_hs : p.k_hs) + l * 8));
     }
   }
+  Params q[U];
+  if constexpr (BITS < 16) {
+    uint32_t mine = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) store_vector<T, D, BITS>(p, isv[u], at[u], l, raw[u]);
+    for (int u = 0; u < U; ++u) {
+      uint32_t ends = ends_of<T>(raw[u]);
+#pragma unroll
+      for (int o = LPV / 2; o; o >>= 1) ends = max_pair<T>(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+      if (l % U == u) mine = ends;
+    }
+    // the vectors' divisions, each by another lane of its threads
+    const Params own = params_of<T, BITS>(mine);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      q[u].s = __shfl_sync(0xffffffffu, own.s, u, LPV);
+      q[u].inv = __shfl_sync(0xffffffffu, own.inv, u, LPV);
+      q[u].z = __shfl_sync(0xffffffffu, own.z, u, LPV);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) store_vector<T, D, BITS>(p, isv[u], at[u], l, raw[u], q[u]);
 }
 
 template <typename T, int D, int BITS, int U>
@@ -238,9 +317,19 @@ __global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs 
       *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(w[u]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t c = (w[u][i * BITS / 32] >> (i * BITS % 32)) & ((1u << BITS) - 1u);
-        out[i] = kc16<T>(scale[u] * (__uint_as_float(0x4B000000u | c) - zero[u]));  // the difference is exact
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t v = w[u][i * BITS / 32] >> (i * BITS % 32);
+        float2 f;  // 2^23 + code
+        if constexpr (BITS == 8) {
+          f.x = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650u));
+          f.y = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651u));
+        } else {
+          f.x = __uint_as_float((v & 15u) | 0x4B000000u);
+          f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
+        }
+        f = mul2(both(scale[u]), add2(f, both(-zero[u])));  // the difference is exact
+        out[i] = kc16<T>(f.x);
+        out[i + 1] = kc16<T>(f.y);
       }
     }
     *reinterpret_cast<uint4*>(static_cast<T*>(isv[u] ? p.vo : p.ko) + to[u] * D + l * 8) =
