@@ -222,9 +222,9 @@ __device__ __forceinline__ void store_vector(const CacheArgs& p, bool isv, int64
   }
 }
 
-// U vectors per thread, loads before anything that waits for them: a thread's two loads depend on one another
-// (slot, then vector), so that one vector per thread leaves the memory idle (8192 x 32 vectors of 128: 137 us
-// to write and read in 4 bits).  Few vectors: one per thread, for the shortest way through.
+// U tokens per thread, of one side and head, so that addresses cost one addition each; loads before anything
+// that waits for them: a thread's two loads depend on one another (slot, then vector).  Few vectors: one per
+// thread, for the shortest way through.
 template <typename T, int D, int BITS, int U>
 __global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs p) {
   constexpr int LPV = D / 8;             // threads of a vector
@@ -232,22 +232,24 @@ __global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs
   const int l = threadIdx.x % LPV;
   int64_t at[U];
   uint4 raw[U];
-  bool isv[U];
-  // (token, side, head): the LPV threads of a vector never cross a warp
+  // (tokens, side, head): the LPV threads of a vector never cross a warp
+  int sh;
+  const int64_t t = static_cast<int64_t>(token_of(p, blockIdx.x * VPC + threadIdx.x / LPV, sh)) * U;
+  const bool isv = sh >= p.heads;
+  const int h = isv ? sh - p.heads : sh;
+  const int64_t step = isv ? p.v_ts : p.k_ts;
+  const T* src = static_cast<const T*>(isv ? p.v : p.k) + t * step + h * (isv ? p.v_hs : p.k_hs) + l * 8;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    int sh;
-    const int64_t t = token_of(p, (blockIdx.x * U + u) * VPC + threadIdx.x / LPV, sh);
-    isv[u] = sh >= p.heads;
-    const int h = isv[u] ? sh - p.heads : sh;
-    at[u] = -1;
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (t < p.count) {
-      at[u] = vector_at(p, __ldg(p.slots + t), h);
-      raw[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(isv[u] ? p.v : p.k) +
-                                                    t * (isv[u] ? p.v_ts : p.k_ts) + h * (isv[u] ? p.v_hs : p.k_hs) + l * 8));
+    at[u] = -1;
+    if (t + u < p.count) {
+      at[u] = __ldg(p.slots + t + u);
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(src + u * step));
     }
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) at[u] = vector_at(p, static_cast<int>(at[u]), h);
   Params q[U];
   if constexpr (BITS < 16) {
     uint32_t mine = 0;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(KC_THREADS) cache_write_kernel(const CacheArgs
     }
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) store_vector<T, D, BITS>(p, isv[u], at[u], l, raw[u], q[u]);
+  for (int u = 0; u < U; ++u) store_vector<T, D, BITS>(p, isv, at[u], l, raw[u], q[u]);
 }
 
 template <typename T, int D, int BITS, int U>
@@ -277,17 +279,17 @@ __global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs 
   constexpr int VPC = KC_THREADS / LPV;
   constexpr int W = BITS / 4;  // words of a thread's 8 values
   const int l = threadIdx.x % LPV;
-  int64_t to[U], at[U];
-  bool isv[U];
+  int64_t at[U];
+  int sh;
+  const int64_t t = static_cast<int64_t>(token_of(p, blockIdx.x * VPC + threadIdx.x / LPV, sh)) * U;
+  const bool isv = sh >= p.heads;
+  const int h = isv ? sh - p.heads : sh;
+  T* dst = static_cast<T*>(isv ? p.vo : p.ko) + (t * p.heads + h) * D + l * 8;
+  const int step = p.heads * D;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    int sh;
-    const int64_t t = token_of(p, (blockIdx.x * U + u) * VPC + threadIdx.x / LPV, sh);
-    isv[u] = sh >= p.heads;
-    const int h = isv[u] ? sh - p.heads : sh;
-    to[u] = t < p.count ? t * p.heads + h : -1;
-    at[u] = t < p.count ? vector_at(p, __ldg(p.slots + t), h) : -1;
-  }
+  for (int u = 0; u < U; ++u) at[u] = t + u < p.count ? __ldg(p.slots + t + u) : -1;
+#pragma unroll
+  for (int u = 0; u < U; ++u) at[u] = vector_at(p, static_cast<int>(at[u]), h);
   uint32_t w[U][W];
   float scale[U], zero[U];
 #pragma unroll
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs 
     scale[u] = 0.f;  // outside the cache: zeros
     zero[u] = 8388608.f;
     if (at[u] < 0) continue;
-    const uint8_t* from = static_cast<const uint8_t*>(isv[u] ? p.vc : p.kc) + at[u] * (D * BITS / 8) + l * BITS;
+    const uint8_t* from = static_cast<const uint8_t*>(isv ? p.vc : p.kc) + at[u] * (D * BITS / 8) + l * BITS;
     if constexpr (W == 4) {
       *reinterpret_cast<uint4*>(w[u]) = __ldg(reinterpret_cast<const uint4*>(from));
     } else {
@@ -305,13 +307,13 @@ __global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs 
         *reinterpret_cast<uint2*>(w[u]) = __ldg(reinterpret_cast<const uint2*>(from));
       else
         w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(from));
-      scale[u] = __ldg((isv[u] ? p.vs : p.ks) + at[u]);
-      zero[u] = __uint_as_float(0x4B000000u | __ldg((isv[u] ? p.vz : p.kz) + at[u]));  // 2^23 + zero
+      scale[u] = __ldg((isv ? p.vs : p.ks) + at[u]);
+      zero[u] = __uint_as_float(0x4B000000u | __ldg((isv ? p.vz : p.kz) + at[u]));  // 2^23 + zero
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (to[u] < 0) continue;
+    if (t + u >= p.count) break;
     alignas(16) T out[8];
     if constexpr (BITS == 16) {
       *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(w[u]);
@@ -332,15 +334,14 @@ __global__ void __launch_bounds__(KC_THREADS) cache_read_kernel(const CacheArgs 
         out[i + 1] = kc16<T>(f.y);
       }
     }
-    *reinterpret_cast<uint4*>(static_cast<T*>(isv[u] ? p.vo : p.ko) + to[u] * D + l * 8) =
-        *reinterpret_cast<const uint4*>(out);
+    *reinterpret_cast<uint4*>(dst + u * step) = *reinterpret_cast<const uint4*>(out);
   }
 }
 
 template <typename T, int D, int U>
 void launch_cache(const CacheArgs& a, int bits, bool write, cudaStream_t s) {
-  constexpr int VPC = U * (KC_THREADS / (D / 8));
-  const unsigned grid = static_cast<unsigned>((a.count * 2 * a.heads + VPC - 1) / VPC);
+  constexpr int VPC = KC_THREADS / (D / 8);
+  const unsigned grid = static_cast<unsigned>(((a.count + U - 1) / U * 2 * a.heads + VPC - 1) / VPC);
   if (write) {
     if (bits == 16)
       cache_write_kernel<T, D, 16, U><<<grid, KC_THREADS, 0, s>>>(a);
