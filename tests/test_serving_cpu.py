@@ -175,3 +175,20 @@ def test_binding_rejections(L):
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_step_batch():
+    from post_weight_quantization_layer_b200 import serving
+
+    b = serving.step_batch([[5, 2], [7], []], [15, 3, 0], [2, 1, 0], 16, device="cpu", width=3)
+    assert b.positions.tolist() == [15, 16, 3] and b.slots.tolist() == [95, 32, 115]
+    assert b.page_table.tolist() == [[5, 2, 0], [7, 0, 0], [0, 0, 0]]
+    assert b.kv_lens.tolist() == [17, 4, 0] and b.q_starts.tolist() == [0, 2, 3, 3] and b.max_q_len == 2
+    assert all(t.dtype == torch.int32 for t in (b.positions, b.slots, b.page_table, b.kv_lens, b.q_starts))
+    for bad in (([[5]], [15], [2]), ([[5]], [-1], [1]), ([[5]], [0], [1, 1])):
+        with pytest.raises(ValueError):
+            serving.step_batch(*bad, 16, device="cpu")
+    with pytest.raises(ValueError):
+        serving.step_batch([[5, 2]], [0], [1], 16, device="cpu", width=1)
+    empty = serving.step_batch([], [], [], 16, device="cpu")
+    assert empty.page_table.shape == (0, 1) and empty.q_starts.tolist() == [0] and empty.max_q_len == 0
