@@ -13,8 +13,10 @@
 //    16-bit operands.  Registers move from the last two to the first.
 //  * 16-bit pages come by TMA straight into the swizzled operand tiles.  Pages of codes come by bulk
 //    copies (codes, scales and zeros of a page and head are contiguous) into a staging ring, from
-//    which the converters write operand tiles, each value rounded once to 16 bits (as cache_read
-//    gives it).
+//    which the converters write operand tiles, each value rounded once: values to q's type (as cache_read
+//    gives them), keys to float16, with the queries of a bfloat16 call, since the scores' error is what the
+//    rounding of keys makes of it (16384 keys of 8 bits, outputs off by 0.0028 of their size instead of 0.0044).
+//    What does not fit float16 becomes infinite and is found by the second look.
 //  * The running maximum moves only when it grows by more than 8 (base 2): until then probabilities
 //    reach 2^8 at most, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
 //  * The (row tile, 128 keys) units of the batch are cut into equal shares, one per SM, as in the
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       // -------------------------------------------------------------- issue of the matrix products
       // The whole warp walks the loops and one elected lane issues: descriptors then stay in uniform
       // registers (a product issues every 66 cycles; from a single lane's branch every 82, measured alone).
-      constexpr uint32_t iqk = instr_desc(FMT, false, false, 128, CH_KEYS);
+      constexpr uint32_t iqk = instr_desc(BITS == 16 ? FMT : 0u, false, false, 128, CH_KEYS);
       constexpr uint32_t ipv = instr_desc(FMT, false, true, 128, D);
       const bool lead = elect_one();
       Ring<C::NST> ring;
@@ -882,6 +884,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (BITS < 16 && !std::is_same<T, __half>::value) {  // float16, as the keys
+#pragma unroll 4
+          for (int r = lane / LPR; r < 128; r += RPI) {
+            uint4* at = reinterpret_cast<uint4*>(qs + chunk_off(r, c));
+            uint4 v = *at;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e[x] = pack2<__half>(__uint_as_float(e[x] << 16), __uint_as_float(e[x] & 0xffff0000u));
+            *at = v;
+          }
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.qfull[w]);
@@ -951,7 +964,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                   f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
                 }
                 f = mul2(add2(f, z2), s2);
-                out[e] = pack2<T>(f.x, f.y);
+                out[e] = kv ? pack2<T>(f.x, f.y) : pack2<__half>(f.x, f.y);
               }
               // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
               const int r = r0 + x * STEP;

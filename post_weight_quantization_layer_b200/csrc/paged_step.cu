@@ -11,6 +11,22 @@
 //  * A lane's operands come from there without rearranging: the order of the contraction index is free as
 //    long as both operands agree, so a lane takes contiguous 16-byte pieces of a key and the query is laid out
 //    to match; for the values the column order is free, and a lane takes contiguous pieces of four keys.
+//  * Codes enter the products as float16 numbers: exact, and without a conversion of their own (1024 + code
+//    is 0x6400 | code, 64 + code of a nibble in bits 4-7 is 0x5400 | bits: a byte permutation or one logical
+//    operation per pair).  Values have 1024 + zero subtracted (exactly) before they are multiplied: their sum over
+//    a long context is small, and an offset taken off after it left 0.39 of it wrong at 131072 keys of 4 bits.
+//    Keys keep their offset, which a contraction over one head affords: q . (c - z) = q . (o + c) - (o + z) sum(q).
+//    A key's scale multiplies its scores, a value's scale its probability: no value is rounded.  The query is
+//    brought into float16's range by a power of two per row, and the weights w_j = p_j scale_j are held against
+//    their own running maximum, so that float16 (2^-11) holds them whatever the scales are.  Converting
+//    pair by pair to 16 bits through fp32 instead took 44 instructions per key and head of 128 and kept the
+//    cache's bytes waiting (64 users, 8 bits: 196 us).
+//  * Each warp has its own ring of steps in shared memory, filled by asynchronous copies two to seven steps
+//    ahead (about 25 KB a warp, 200 KB an SM): the bytes in flight that the memory's latency asks for do not
+//    fit in registers (prefetching there: 32 KB an SM, 8-bit cache at 3.4 TB/s).
+//  * A lane's operands come from there without rearranging: the order of the contraction index is free as
+//    long as both operands agree, so a lane takes contiguous 16-byte pieces of a key and the query is laid out
+//    to match; for the values the column order is free, and a lane takes contiguous pieces of four keys.
 //  * Codes enter the products as the float16 numbers 1024 + code (0x6400 | code: a byte permutation or one
 //    logical operation per pair), and what that adds is taken off afterwards:
 //      q . (c - z) = q . (1024 + c) - (1024 + z) sum(q),
@@ -149,12 +165,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Codes as pairs of halves: 1024 + code, or 1024 + 16 code of the upper nibbles of a byte, which come without
-// a shift; what meets them is divided by 16.
+// Codes as pairs of halves: 1024 + code of bytes, 64 + code of nibbles in bits 4-7 of each half (keys); of
+// values 1024 + code, or 1024 + 16 code for the upper nibbles of a byte, which come without a shift.
 __device__ __forceinline__ uint32_t low_bytes(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4140u); }
 __device__ __forceinline__ uint32_t high_bytes(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4342u); }
+__device__ __forceinline__ uint32_t key_nibbles(uint32_t w) { return (w & 0x00f000f0u) | 0x54005400u; }
 __device__ __forceinline__ uint32_t low_nibbles(uint32_t w) { return (w & 0x000f000fu) | 0x64006400u; }
 __device__ __forceinline__ uint32_t high_nibbles(uint32_t w) { return (w & 0x00f000f0u) | 0x64006400u; }
+__device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
 
 // An 8 x 8 matrix of 16-bit values, a row of pairs per four lanes, turned round.
 __device__ __forceinline__ uint32_t turned(uint32_t w) {
@@ -194,7 +215,7 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
     // a lane holds the query of row g (of each 8) as an operand and the scores of rows 2t, 2t + 1.
     uint32_t qf[NR][D / 16][2];
     int see[NR][2], least = k1;
-    float power[NR][2], qsum[NR][2], qoff[NR][2];  // for codes: see below
+    float power[NR][2], qsum[NR][2];  // for codes: see below
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int row = 8 * r + g;
@@ -209,9 +230,9 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
         raw[kk] = make_uint4(0, 0, 0, 0);
         if (in) raw[kk] = __ldg(reinterpret_cast<const uint4*>(qr + key_elem<D, BITS>(t, kk)));
       }
-      float up = 1.f, sum = 0.f, base = 0.f;
+      float up = 1.f, sum = 0.f;
       if constexpr (BITS < 16) {
-        // the row over a power of two, in float16, its sum, and what the codes' offsets make of it
+        // the row over a power of two, in float16, and its sum
         float top = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk)
@@ -228,19 +249,13 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const T* v = reinterpret_cast<const T*>(&raw[kk]) + 2 * e;
-            // 4 bits: the codes of odd elements come 16 times as large
-            w[e] = __floats2half2_rn(to_f32(v[0]) * down, to_f32(v[1]) * (BITS == 4 ? down * 0.0625f : down));
-            const float x = __low2float(w[e]), y = __high2float(w[e]);
-            sum += x + (BITS == 4 ? 16.f * y : y);
-            base += x + y;
+            w[e] = __floats2half2_rn(to_f32(v[0]) * down, to_f32(v[1]) * down);
+            sum += __low2float(w[e]) + __high2float(w[e]);
           }
           raw[kk] = *reinterpret_cast<const uint4*>(w);
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          base += __shfl_xor_sync(0xffffffffu, base, o);
-        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       }
 #pragma unroll
       for (int kk = 0; kk < D / 32; ++kk) {
@@ -264,7 +279,6 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
         if constexpr (BITS < 16) {
           power[r][c] = __shfl_sync(0xffffffffu, up, from);
           qsum[r][c] = __shfl_sync(0xffffffffu, sum, from);
-          qoff[r][c] = 1024.f * __shfl_sync(0xffffffffu, base, from);
         }
       }
     }
@@ -278,12 +292,12 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
     // Running maximum and sum.  For codes also the running maximum of the weights (base 2), which the weighted
-    // sum is held against, and what the codes' offsets add to it.
-    float m[NR][2], l[NR][2], mw[NR][2], off[NR][4];
+    // sum is held against.
+    float m[NR][2], l[NR][2], mw[NR][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       m[r][0] = m[r][1] = mw[r][0] = mw[r][1] = -INFINITY;
-      l[r][0] = l[r][1] = off[r][0] = off[r][1] = off[r][2] = off[r][3] = 0.f;
+      l[r][0] = l[r][1] = 0.f;
     }
 
     int64_t vecn[NK];  // first vector of each 16 keys of the step to be loaded next
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[kk][r][e] = BITS < 16 ? -qoff[r][e & 1] : 0.f;
+          for (int e = 0; e < 4; ++e) sc[kk][r][e] = BITS < 16 ? (BITS == 8 ? -1024.f : -64.f) * qsum[r][e & 1] : 0.f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t f[4];
@@ -380,11 +394,11 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
             f[2] = high_bytes(ka[ks]);
             f[3] = high_bytes(kb[ks]);
           } else {
-            const uint32_t x = ka[ks >> 1] >> ((ks & 1) * 8), y = kb[ks >> 1] >> ((ks & 1) * 8);
-            f[0] = low_nibbles(x);
-            f[1] = low_nibbles(y);
-            f[2] = high_nibbles(x);
-            f[3] = high_nibbles(y);
+            const uint32_t x = ka[ks >> 1], y = kb[ks >> 1];
+            f[0] = key_nibbles((ks & 1) ? x >> 4 : x << 4);
+            f[1] = key_nibbles((ks & 1) ? y >> 4 : y << 4);
+            f[2] = key_nibbles((ks & 1) ? x >> 8 : x);
+            f[3] = key_nibbles((ks & 1) ? y >> 8 : y);
           }
 #pragma unroll
           for (int r = 0; r < NR; ++r) mma<PT>(sc[kk][r], f, qf[r][ks][0], qf[r][ks][1]);
@@ -445,8 +459,6 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
             if constexpr (BITS < 16) {
               f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - mwx[r][c]);
               mw[r][c] = mwx[r][c];
-              off[r][c] *= f;
-              off[r][2 + c] *= f;
             }
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
@@ -496,11 +508,13 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
               for (int e = 0; e < Y::VW; ++e) vw[x][r][e] = 0;
             }
           }
-        if constexpr (BITS < 16) {  // the offsets' columns: 1024 + zero, and for 4 bits 1024
-          const uint32_t lo = low_bytes(vz[kk][0]), hi = low_bytes(vz[kk][1]);
-          const uint32_t f[4] = {lo, BITS == 4 ? 0x64006400u : lo, hi, BITS == 4 ? 0x64006400u : hi};
-#pragma unroll
-          for (int r = 0; r < NR; ++r) mma<PT>(off[r], f, pf[kk][r][0], pf[kk][r][1]);
+        // 1024 + zero of the four keys, and 1024 + 16 zero
+        uint32_t z0 = 0, z1 = 0, y0 = 0, y1 = 0;
+        if constexpr (BITS < 16) {
+          z0 = low_bytes(vz[kk][0]);
+          z1 = low_bytes(vz[kk][1]);
+          y0 = ((z0 & 0x000f000fu) << 4) | 0x64006400u;
+          y1 = ((z1 & 0x000f000fu) << 4) | 0x64006400u;
         }
         auto add = [&](int i, uint32_t f0, uint32_t f1, uint32_t f2, uint32_t f3) {
           const uint32_t f[4] = {f0, f1, f2, f3};
@@ -519,13 +533,14 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
               if constexpr (BITS == 8) {
                 const uint32_t sel = hf ? 0x7362u : 0x5140u;  // bytes 2 hf, 2 hf + 1 of both keys
                 const uint32_t x = __byte_perm(a0, a1, sel), y = __byte_perm(b0, b1, sel);
-                add(2 * w + hf, low_bytes(x), high_bytes(x), low_bytes(y), high_bytes(y));
+                add(2 * w + hf, less(low_bytes(x), z0), less(high_bytes(x), z0), less(low_bytes(y), z1), less(high_bytes(y), z1));
               } else {
                 const uint32_t sel = hf ? 0x7632u : 0x5410u;
                 const uint32_t x = __byte_perm(a0, a1, sel), y = __byte_perm(b0, b1, sel);
-                add(4 * w + 2 * hf, low_nibbles(x), high_nibbles(x), low_nibbles(y), high_nibbles(y));
-                add(4 * w + 2 * hf + 1, low_nibbles(x >> 8), high_nibbles(x >> 8), low_nibbles(y >> 8),
-                    high_nibbles(y >> 8));
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  add(4 * w + 2 * hf + b, less(low_nibbles(x >> (8 * b)), z0), less(high_nibbles(x >> (8 * b)), y0),
+                      less(low_nibbles(y >> (8 * b)), z1), less(high_nibbles(y >> (8 * b)), y1));
               }
             }
           }
@@ -540,13 +555,12 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int row = 8 * r + 2 * t + c;
-        if constexpr (BITS < 16) {  // offsets off, and back to the row's own maximum
+        if constexpr (BITS < 16) {  // back to the row's own maximum; upper nibbles came 16 times as large
           const float f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - m[r][c]);
-          const float off1 = BITS == 4 ? off[r][2 + c] + 16.f * (off[r][c] - off[r][2 + c]) : off[r][c];
 #pragma unroll
           for (int i = 0; i < NO; ++i) {
-            o[r][i][c] = (o[r][i][c] - off[r][c]) * f;
-            o[r][i][2 + c] = (o[r][i][2 + c] - off1) * (BITS == 4 ? f * 0.0625f : f);
+            o[r][i][c] *= f;
+            o[r][i][2 + c] *= BITS == 4 ? f * 0.0625f : f;
           }
         }
 #pragma unroll

@@ -271,6 +271,38 @@ def test_attention_counts_every_key_once(bits, group, D, have, new):
         at += n
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("n", [1, 24])
+def test_attention_long_context(dtype, bits, n):
+    """60000 keys that weigh much the same: the answer is some 200 times smaller than the values, and
+    errors that grow with the number of keys or with an offset of the codes would show.  Roundings here are
+    many and independent: the 2-norm of the error is held to 4 times the quadrature sum of the relative errors'
+    spreads, u / sqrt(3) of the probability, of values and keys behind codes (the scores' error is theirs times
+    their spread, below 2 here), and of the output."""
+    D, L, group = 128, 60001, 4
+    g = torch.Generator().manual_seed(bits)
+
+    def kv(s, L):
+        return (0.7 * torch.randn(L, 1, D, generator=g)).to(dtype), torch.randn(L, 1, D, generator=g).to(dtype)
+
+    c = _case([L], [n], 1, D, 64, bits, dtype, 3, kv=kv, Hq=group)
+    out = _np(_attend(c, bits))
+    k, v = c["vals"][0]
+    q = _np(c["q"])
+    ref = np.empty_like(q)
+    for i in range(n):
+        m = L - n + i + 1
+        s = q[i] @ k[:m, 0].T / np.sqrt(D)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        ref[i] = p @ v[:m, 0] / p.sum(-1, keepdims=True)
+    u = U[dtype]
+    up = max(u, 2.0 ** -8) if bits < 16 else u
+    codes = (u * 2, u) if bits < 16 else (0.0, 0.0)
+    most = 4 * np.sqrt((u ** 2 + up ** 2 + codes[0] ** 2 + codes[1] ** 2) / 3)
+    assert np.linalg.norm(out - ref) <= most * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("bits", [16, 8, 4])
 @pytest.mark.parametrize("n", [1, 2, 200])
 def test_attention_finds_the_key(bits, n):
