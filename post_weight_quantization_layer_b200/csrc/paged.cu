@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(JN_THREADS) join_kernel(const Args a, const fl
 int attend(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s) {
   const bool chunks = static_cast<int64_t>(a.max_q) * a.group > kStepRows;
   const bool steps = a.group <= kStepRows;  // sequences with few rows may be among long ones
-  bool step_cuts = false;
-  const int step_ctas = steps ? step_grid(a, &step_cuts) : 0;
-  const int step_n = step_cuts ? step_ctas : 0, chunk_n = chunks ? num_sms() : 0;
+  int team = 1;
+  const int step_ctas = steps ? step_grid(a, &team) : 0;
+  const int step_n = team == 0 ? step_ctas : 0, chunk_n = chunks ? num_sms() : 0;
   const size_t step_bytes = static_cast<size_t>(step_n) * (2 * step_part(head_dim) * sizeof(float) + sizeof(Cut));
   const size_t chunk_bytes =
       static_cast<size_t>(chunk_n) * (2 * chunk_part(head_dim) * sizeof(float) + sizeof(Cut) + sizeof(int));
@@ -109,7 +109,7 @@ int attend(const Args& a, int dtype, int head_dim, int bits, cudaStream_t s) {
   Cut* step_cut = chunk_cut + chunk_n;
   int* odd = reinterpret_cast<int*>(step_cut + step_n);
   int st = GPTQ_OK;
-  if (steps) st = run_step(a, dtype, head_dim, bits, step_ctas, step_cuts, step_parts, step_cut, s);
+  if (steps) st = run_step(a, dtype, head_dim, bits, step_ctas, team, step_parts, step_cut, s);
   if (st == GPTQ_OK && chunks)
     st = run_chunk(a, dtype, head_dim, bits, chunk_n, chunk_parts, chunk_cut, odd, steps, s);
   const int step_borders = step_n > 1 ? step_n - 1 : 0, chunk_borders = chunk_n > 1 ? chunk_n - 1 : 0;

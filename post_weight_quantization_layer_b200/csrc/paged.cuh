@@ -184,12 +184,12 @@ __device__ __forceinline__ Cut cut_at(int64_t at, int64_t per, int skipped, int 
   return c;
 }
 
-// paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).  step_grid: CTAs, and whether
-// items can be cut; a part of a cut item is step_part(head_dim) floats.
+// paged_step.cu: the sequences with 1 .. 16 rows (tokens x heads of a kv head).  step_grid: CTAs, and how many take
+// an item together (0: items are cut; a part of a cut item is step_part(head_dim) floats).
 constexpr int kStepRows = 16;
 __host__ __device__ constexpr int step_part(int d) { return kStepRows * (d + 2); }
-int step_grid(const Args& a, bool* cuts);
-int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s);
+int step_grid(const Args& a, int* team);
+int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, int team, float* part, Cut* cut, cudaStream_t s);
 
 // paged_chunk.cu: the sequences with more rows, in tiles of kTileRows.  odd: a word per CTA, not 0 where it met
 // a result that is not finite.  `next`: follows a launch of the same call.

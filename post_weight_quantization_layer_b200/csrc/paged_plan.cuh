@@ -10,7 +10,7 @@ namespace paged {
 
 struct Share {
   int grid;
-  int whole;             // no cutting: CTA c takes items c, c + grid, ...
+  int whole;             // not 0: no cutting, teams of so many CTAs (a cluster) take whole items
   int min_per;           // least units of a share
   int rows_lo, rows_hi;  // the sequences taken: rows (tokens x heads of a kv head) in this range
 };
@@ -55,12 +55,13 @@ __device__ __forceinline__ int64_t share_of(const Share& sh, int64_t line) {
 }
 
 __device__ __forceinline__ void set_whole(const Args& a, const Share& sh, int unit, Cursor& c) {
-  for (; c.at < c.end; c.at += sh.grid) {
+  const int rank = blockIdx.x % sh.whole;
+  for (; c.at < c.end; c.at += sh.grid / sh.whole) {
     c.s = static_cast<int>(c.at / a.kv_heads);
     c.head = static_cast<int>(c.at - static_cast<int64_t>(c.s) * a.kv_heads);
     c.units = units_of(a, sh, unit, c.s);
-    c.u0 = 0;
-    c.u1 = c.units;
+    c.u0 = static_cast<int>(static_cast<int64_t>(c.units) * rank / sh.whole);
+    c.u1 = static_cast<int>(static_cast<int64_t>(c.units) * (rank + 1) / sh.whole);
     if (c.units) return;
   }
 }
@@ -70,7 +71,7 @@ template <int THREADS>
 __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c, Cursor* shared) {
   __shared__ int64_t ws[THREADS / 32];
   if (sh.whole) {
-    c.at = blockIdx.x;
+    c.at = blockIdx.x / sh.whole;
     c.end = static_cast<int64_t>(a.seqs) * a.kv_heads;
     set_whole(a, sh, unit, c);
     return c.at < c.end;
@@ -118,7 +119,7 @@ __device__ bool first_piece(const Args& a, const Share& sh, int unit, Cursor& c,
 
 __device__ __forceinline__ void next_piece(const Args& a, const Share& sh, int unit, Cursor& c) {
   if (sh.whole) {
-    c.at += sh.grid;
+    c.at += sh.grid / sh.whole;
     set_whole(a, sh, unit, c);
     return;
   }

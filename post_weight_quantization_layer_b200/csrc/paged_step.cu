@@ -177,6 +177,26 @@ __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
+// The shared memory of the CTAs of a cluster.
+__device__ __forceinline__ void team_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(uint32_t at, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_float(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_float4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 // An 8 x 8 matrix of 16-bit values, a row of pairs per four lanes, turned round.
 __device__ __forceinline__ uint32_t turned(uint32_t w) {
   uint32_t r;
@@ -601,8 +621,10 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
         __syncthreads();
       }
     }
-    const bool whole = cur.u0 == 0 && cur.u1 == cur.units;
-    float* mine = whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (cur.at == first ? 0 : 1)) * step_part(D);
+    const bool whole = sh.whole || (cur.u0 == 0 && cur.u1 == cur.units);
+    const int team = sh.whole ? sh.whole : 1;
+    float* both = reinterpret_cast<float*>(smem + Y::PART);  // this CTA's part, for its team
+    float* mine = team > 1 ? both : whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + (cur.at == first ? 0 : 1)) * step_part(D);
     for (int e = threadIdx.x; e < rows * (D / 4); e += ST_THREADS) {
       const int row = e / (D / 4), c = (e % (D / 4)) * 4;
       float mm = -INFINITY;
@@ -624,8 +646,8 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
       if (mine) {
         *reinterpret_cast<float4*>(mine + row * D + c) = v;
         if (c == 0) {
-          mine[16 * D + row] = mm;
-          mine[16 * D + 16 + row] = ll;
+          mine[kStepRows * D + row] = mm;
+          mine[kStepRows * (D + 1) + row] = ll;
         }
       } else {
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
@@ -638,6 +660,53 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
         *reinterpret_cast<uint2*>(dst) = w;
       }
     }
+    if (team > 1) {
+      // The team's parts, read from the shared memory of its CTAs, each of which joins its share of the columns, in
+      // the order of the keys.
+      team_barrier();
+      const int rank = blockIdx.x % team;
+      const uint32_t from = static_cast<uint32_t>(__cvta_generic_to_shared(both));
+      for (int e = rank * ST_THREADS + threadIdx.x; e < rows * (D / 4); e += team * ST_THREADS) {
+        const int row = e / (D / 4), c = (e % (D / 4)) * 4;
+        float pm[8], pl[8];
+        float4 y[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          pm[x] = -INFINITY;
+          pl[x] = 0.f;
+          y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (x >= team) continue;
+          const uint32_t there = peer(from, x);
+          pm[x] = peer_float(there + (kStepRows * D + row) * 4);
+          pl[x] = peer_float(there + (kStepRows * (D + 1) + row) * 4);
+          y[x] = peer_float4(there + (row * D + c) * 4);
+        }
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) mm = fmaxf(mm, pm[x]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          if (x >= team) continue;
+          const float f = ex2(pm[x] - ref);
+          ll += f * pl[x];
+          v.x += f * y[x].x;
+          v.y += f * y[x].y;
+          v.z += f * y[x].z;
+          v.w += f * y[x].w;
+        }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        const int i = row / a.group;
+        T* dst = static_cast<T*>(a.out) +
+                 ((static_cast<int64_t>(q.start) + i) * a.heads + h * a.group + (row - i * a.group)) * D + c;
+        uint2 w;
+        w.x = pack2<T>(v.x * inv, v.y * inv);
+        w.y = pack2<T>(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(dst) = w;
+      }
+      team_barrier();  // nobody leaves, or goes on, while its part is read
+    }
     __syncthreads();
   }
 }
@@ -645,45 +714,70 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
 // No sequence of the call has more than 8 rows here: half the products and registers.
 bool eight(const Args& a) { return static_cast<int64_t>(a.max_q) * a.group <= 8; }
 
-// Contexts of a few units are not cut: a piece per CTA, nothing to join.
-constexpr int ST_WHOLE = 8;
-
 template <typename T, int D, int BITS, int NR>
-int run(const Args& a, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s) {
+int run(const Args& a, int grid, int team, float* part, Cut* cut, cudaStream_t s) {
   using Y = Lay<D, BITS, NR>;
   constexpr int smem = 4 * Y::RING + 2 * 4 * 16 * static_cast<int>(sizeof(float));
   static_assert(Y::STAGES >= 2 && Y::CTAS * (smem + 1024 + 256) <= 233472, "the CTAs of an SM share its memory");
   GPTQ_TRY(ensure_smem_limit(reinterpret_cast<const void*>(step_kernel<T, D, BITS, NR>), smem));
   Share sh;
-  sh.whole = !cuts;
+  sh.whole = team;
   sh.min_per = 4;
   sh.rows_lo = 1;
   sh.rows_hi = kStepRows;
   sh.grid = grid;
-  step_kernel<T, D, BITS, NR><<<grid, ST_THREADS, smem, s>>>(a, sh, part, cuts ? cut : nullptr);
+  static_assert(Y::PART + step_part(D) * 4 <= Y::RING, "a team's parts lie behind the first warp's");
+  if (team > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(ST_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = team;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, step_kernel<T, D, BITS, NR>, a, sh, part, static_cast<Cut*>(nullptr)) != cudaSuccess) {
+      cudaGetLastError();
+      return GPTQ_ERR_CUDA;
+    }
+    return after_launch();
+  }
+  step_kernel<T, D, BITS, NR><<<grid, ST_THREADS, smem, s>>>(a, sh, part, team == 0 ? cut : nullptr);
   return after_launch();
 }
 
 template <typename T, int D, int BITS>
-int run(const Args& a, int grid, bool cuts, float* part, Cut* cut, cudaStream_t s) {
-  return eight(a) ? run<T, D, BITS, 1>(a, grid, cuts, part, cut, s) : run<T, D, BITS, 2>(a, grid, cuts, part, cut, s);
+int run(const Args& a, int grid, int team, float* part, Cut* cut, cudaStream_t s) {
+  return eight(a) ? run<T, D, BITS, 1>(a, grid, team, part, cut, s) : run<T, D, BITS, 2>(a, grid, team, part, cut, s);
 }
 
 }  // namespace
 
-int step_grid(const Args& a, bool* cuts) {
+// Few items of short contexts: a cluster of CTAs per item, which join their parts through shared memory, without
+// the line's scan and a second launch.  Long contexts and many items: the line, whose shares are even.  Contexts of
+// a few units: an item per CTA.
+int step_grid(const Args& a, int* team) {
   const int64_t units = ((a.table_width << a.page_shift) + ST_UNIT - 1) / ST_UNIT;
   const int64_t items = static_cast<int64_t>(a.seqs) * a.kv_heads;
-  *cuts = units > ST_WHOLE;
-  return static_cast<int>(*cuts ? std::min<int64_t>(items * units, (eight(a) ? 3 : 2) * num_sms()) : std::min<int64_t>(items, 1 << 20));
+  const int64_t slots = static_cast<int64_t>(eight(a) ? 3 : 2) * num_sms();
+  *team = units <= 8 ? 1 : 0;
+  if (units > 2 && units <= 64)
+    for (int x = 2; x <= 8; x *= 2)
+      if (items * x <= slots && x <= units) *team = x;
+  if (*team == 0) return static_cast<int>(std::min(items * units, slots));
+  return static_cast<int>(std::min<int64_t>(items, 1 << 20)) * *team;
 }
 
-int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, bool cuts, float* part, Cut* cut,
+int run_step(const Args& a, int dtype, int head_dim, int bits, int grid, int team, float* part, Cut* cut,
              cudaStream_t s) {
 #define GPTQ_STEP(T, D)                                                                                        \
-  return bits == 16  ? run<T, D, 16>(a, grid, cuts, part, cut, s)                                               \
-         : bits == 8 ? run<T, D, 8>(a, grid, cuts, part, cut, s)                                                \
-                     : run<T, D, 4>(a, grid, cuts, part, cut, s)
+  return bits == 16  ? run<T, D, 16>(a, grid, team, part, cut, s)                                               \
+         : bits == 8 ? run<T, D, 8>(a, grid, team, part, cut, s)                                                \
+                     : run<T, D, 4>(a, grid, team, part, cut, s)
   if (dtype == GPTQ_BF16) {
     if (head_dim == 128) GPTQ_STEP(__nv_bfloat16, 128);
     GPTQ_STEP(__nv_bfloat16, 64);
