@@ -7,12 +7,14 @@ is missing or fails to load, every call raises.  There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "lib", "libgptq.so")
+BINDING_PATH = os.path.join(PKG, "lib", "_binding.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "gptq.h")
 
 _lock = threading.Lock()
@@ -106,6 +108,31 @@ def lib():
                 fn.argtypes = args
             _lib = handle
     return _lib
+
+
+_binding = None
+
+
+def binding():
+    """The native front of the serving operators (csrc/binding.cpp), opened on the native library (raises
+    RuntimeError if it is not built)."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError(f"native binding missing at {BINDING_PATH}; build it with "
+                                   "`python -m post_weight_quantization_layer_b200.build`")
+            import torch  # noqa: F401  (the binding links against its libraries)
+            spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            if not os.path.exists(LIB_PATH):
+                raise RuntimeError(f"native GPTQ library missing at {LIB_PATH}")
+            module.open(LIB_PATH)
+            _binding = module
+    return _binding
 
 
 def declared_symbols():

@@ -1,4 +1,5 @@
-"""Build the native library ``lib/libgptq.so`` in-tree with nvcc for sm_100a.
+"""Build the native library ``lib/libgptq.so`` in-tree with nvcc for sm_100a, and the binding's native front
+``lib/_binding.so`` (host code) with g++.
 
 Usage: ``python -m post_weight_quantization_layer_b200.build`` (or ``build()``).
 Cross-compiles on a machine without a GPU.
@@ -11,11 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libgptq.so")
+BINDING = os.path.join(LIBDIR, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 ROOT = os.path.dirname(PKG)
 
 NVCC_FLAGS = [
@@ -46,22 +50,54 @@ def needs_build():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def binding_needs_build():
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(p) > t for p in [BINDING_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def binding_command(out):
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    abi = int(torch.compiled_with_cxx11_abi())
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+            *(a for i in inc for a in ("-I", i)), BINDING_SRC, "-o", out, "-L", os.path.join(base, "lib"),
+            "-Wl,-rpath," + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile every CUDA source into one shared library; returns its path."""
-    if not force and not needs_build():
+    """Compile every CUDA source into one shared library, and the binding's front; returns the library's
+    path."""
+    jobs = []
+    if force or needs_build():
+        jobs.append((LIB, lambda out: [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"),
+                                       *sources(), "-o", out]))
+    if force or binding_needs_build():
+        jobs.append((BINDING, binding_command))
+    if not jobs:
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"),
-           *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-    if verbose and (res.stdout or res.stderr):
-        print(res.stdout + res.stderr, file=sys.stderr)
-    os.replace(tmp, LIB)
+    running = []
+    for path, command in jobs:  # side by side
+        cmd = command(path + ".tmp")
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        running.append((path, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+    failed = []
+    for path, p in running:
+        out, err = p.communicate()
+        if p.returncode != 0:
+            failed.append(f"{os.path.basename(path)}: compiler failed ({p.returncode}):\n{out}\n{err}")
+        elif verbose and (out or err):
+            print(out + err, file=sys.stderr)
+    if failed:
+        raise RuntimeError("\n".join(failed))
+    for path, _ in running:
+        os.replace(path + ".tmp", path)
     return LIB
 
 

@@ -9,6 +9,10 @@ A cache is a dict of CUDA tensors, made by ``new_cache`` or by the caller:
 Slot s of the cache is row s % page_size of page s // page_size.  A value is
 scale * (code - zero), the form of the library's quantized weights, one scale and zero point per
 token, head and side.
+
+The plain case of each call (outputs made here, the current stream) goes through the native front of
+``csrc/binding.cpp``, which checks, allocates and launches; anything else, and everything that is wrong,
+through the Python below, which says what.
 """
 
 from __future__ import annotations
@@ -18,7 +22,7 @@ import ctypes
 
 import torch
 
-from ._native import lib
+from ._native import binding, lib
 from .api import _DTYPE, _check, _need, _need_cuda
 
 SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -68,6 +72,16 @@ def _device():
 
 def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _six(cache, bits):
+    """A cache's tensors for the native front (which answers None where one is not there)."""
+    if cache.__class__ is not dict:
+        return (None,) * 6
+    get = cache.get
+    if bits == 16:
+        return get("k"), get("v"), None, None, None, None
+    return get("k"), get("v"), get("k_scales"), get("k_zeros"), get("v_scales"), get("v_zeros")
 
 
 def _cache(cache, bits, kv_heads, head_dim, dtype, dev):
@@ -142,6 +156,12 @@ def rotary(q, k, positions, inv_freq, attention_factor=1.0, interleaved=False, o
     `interleaved`, by positions[t] * inv_freq[i]; the rest is copied.  q and k may be strided views
     of a fused projection.  Returns (q, k) as new tensors, or written to out = (q_out, k_out), which
     may be (q, k) themselves."""
+    if out is None and stream is None:
+        r = binding().rotary(q, k, positions, inv_freq, attention_factor, interleaved)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r, "gptq_rotary")
     (T, Hq, D), qt, qh = _heads(q, "q")
     Hk, kt, kh = 0, 0, 0
     if k is not None:
@@ -184,6 +204,12 @@ def cache_write(k, v, cache, slots, bits=16, stream=None):
     """Store k and v [tokens, kv_heads, head_dim] of each token in its slot (int32 [tokens]), quantized
     below 16 bits.  A slot outside the cache (-1 for a padded token) is left out; the others must
     differ.  Returns the cache."""
+    if stream is None:
+        r = binding().cache_write(k, v, *_six(cache, bits), slots, bits)
+        if r is True:
+            return cache
+        if r is not None:
+            _check(r, "gptq_cache_write")
     (T, H, D), kt, kh = _heads(k, "k")
     shape, vt, vh = _heads(v, "v", k.dtype)
     if tuple(shape) != (T, H, D):
@@ -206,6 +232,12 @@ def cache_read(cache, slots, bits=16, dtype=None, stream=None):
         dtype = own if own in (torch.float16, torch.bfloat16) else torch.bfloat16
     if dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("dtype must be float16 or bfloat16")
+    if stream is None:
+        r = binding().cache_read(*_six(cache, bits), slots, bits, dtype is torch.float16)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r, "gptq_cache_read")
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D int32 tensor")
     dev = _device()
@@ -233,6 +265,12 @@ def paged_attention(q, cache, page_table, kv_lens, q_starts, bits=16, max_q_len=
     causal:     row i of n sees the keys 0 .. kv_len - n + i, else all of its sequence's keys
     scale:      of the scores, default head_dim ** -0.5
     Rows that see no key are zeros; rows of no sequence are left as they were in `out`."""
+    if out is None and stream is None:
+        r = binding().paged_attention(q, *_six(cache, bits), page_table, kv_lens, q_starts, bits, max_q_len, causal, scale)
+        if isinstance(r, torch.Tensor):
+            return r
+        if r is not None:
+            _check(r, "gptq_paged_attention")
     (T, Hq, D), qt, qh = _heads(q, "q")
     dev = _device()
     ptrs, pages, P, H, _ = _cache(cache, bits, None, D, q.dtype, dev)
