@@ -148,8 +148,10 @@ extern "C" int gptq_paged_attention(const void* q, int dtype, int64_t tokens, in
   if (work && (!q || !out || !page_table || !kv_lens || !q_starts || table_width <= 0)) return GPTQ_ERR_INVALID_ARG;
   GPTQ_TRY(check_cache(k_cache, v_cache, k_scales, k_zeros, v_scales, v_zeros, bits, pages, page_size, kv_heads,
                        head_dim, dtype));
+  if (work && out == q) return GPTQ_ERR_INVALID_ARG;  // rows are read again after others are written
   if (heads % kv_heads || !(scale > 0.f && scale < INFINITY)) return GPTQ_ERR_INVALID_ARG;
   if (heads / kv_heads > 64 || heads > 65535 || seqs > (1 << 20) || table_width > (int64_t(1) << 27) ||
+      table_width * page_size > (int64_t(1) << 31) - 1024 ||
       tokens * heads > (int64_t(1) << 30))
     return GPTQ_ERR_UNSUPPORTED;
   if (((q_token_stride | q_head_stride) & 7) || !aligned16(q) || !aligned16(out)) return GPTQ_ERR_UNSUPPORTED;

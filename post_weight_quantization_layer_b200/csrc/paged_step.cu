@@ -1,16 +1,19 @@
 // Attention over a paged cache for sequences with few rows (at most 16 rows times heads of a kv
 // head: single tokens, short guesses).
 //
-// Each key and value byte is used for at most 16 rows, so the cache's bytes bound the kernel and
-// everything serves keeping loads in flight:
-//  * The rows of all query heads that share a kv head are one 16-row tile (row i * group + g), so a
-//    cache line is read once.  Scores and the weighted sum run on the 16x8x16 matrix instruction.
-//  * Each warp has its own ring of steps in shared memory, filled by asynchronous copies two to seven steps
-//    ahead (about 25 KB a warp, 200 KB an SM): the bytes in flight that the memory's latency asks for do not
-//    fit in registers (prefetching there: 32 KB an SM, 8-bit cache at 3.4 TB/s).
+// Each key and value byte is used for at most 16 rows, so the cache's bytes bound the kernel, and after
+// them the instructions that codes take (4 bits: half the bytes, the same instructions):
+//  * The rows of all query heads that share a kv head (row i * group + g) are the 8 (or 2 x 8) columns of the
+//    16x8x16 matrix instruction, keys, and then the columns of the values, its 16 rows: a cache line is read
+//    once, and up to 8 rows cost half the products and accumulators of a 16-row tile (64 users of 70B-shaped
+//    heads, 8 bits: 148 -> 118 us; four users, 131072 keys, 4 bits: 249 -> 183 us).
+//  * Each warp has its own ring of steps in shared memory, filled by asynchronous copies one to seven steps
+//    ahead (17 KB a warp, 200 KB an SM): the bytes in flight that the memory's latency asks for do not fit in
+//    registers (prefetching there: 32 KB an SM, 8-bit cache at 3.4 TB/s; now 5.4).
 //  * A lane's operands come from there without rearranging: the order of the contraction index is free as
 //    long as both operands agree, so a lane takes contiguous 16-byte pieces of a key and the query is laid out
-//    to match; for the values the column order is free, and a lane takes contiguous pieces of four keys.
+//    to match; for the values the column order is free, and a lane takes contiguous pieces of four keys.  The
+//    probabilities are turned into an operand by a transposition across the warp.
 //  * Codes enter the products as float16 numbers: exact, and without a conversion of their own (1024 + code
 //    is 0x6400 | code, 64 + code of a nibble in bits 4-7 is 0x5400 | bits: a byte permutation or one logical
 //    operation per pair).  Values have 1024 + zero subtracted (exactly) before they are multiplied: their sum over
@@ -18,30 +21,14 @@
 //    Keys keep their offset, which a contraction over one head affords: q . (c - z) = q . (o + c) - (o + z) sum(q).
 //    A key's scale multiplies its scores, a value's scale its probability: no value is rounded.  The query is
 //    brought into float16's range by a power of two per row, and the weights w_j = p_j scale_j are held against
-//    their own running maximum, so that float16 (2^-11) holds them whatever the scales are.  Converting
-//    pair by pair to 16 bits through fp32 instead took 44 instructions per key and head of 128 and kept the
-//    cache's bytes waiting (64 users, 8 bits: 196 us).
-//  * Each warp has its own ring of steps in shared memory, filled by asynchronous copies two to seven steps
-//    ahead (about 25 KB a warp, 200 KB an SM): the bytes in flight that the memory's latency asks for do not
-//    fit in registers (prefetching there: 32 KB an SM, 8-bit cache at 3.4 TB/s).
-//  * A lane's operands come from there without rearranging: the order of the contraction index is free as
-//    long as both operands agree, so a lane takes contiguous 16-byte pieces of a key and the query is laid out
-//    to match; for the values the column order is free, and a lane takes contiguous pieces of four keys.
-//  * Codes enter the products as the float16 numbers 1024 + code (0x6400 | code: a byte permutation or one
-//    logical operation per pair), and what that adds is taken off afterwards:
-//      q . (c - z) = q . (1024 + c) - (1024 + z) sum(q),
-//      sum_j w_j (c_j - z_j) = sum_j w_j (1024 + c_j) - sum_j w_j (1024 + z_j),
-//    the last sum by one more column of the product.  (Both terms are exact products summed in fp32; their
-//    difference keeps 2^-24 of 1280, against values of up to 255.)  A key's scale multiplies its scores, a
-//    value's scale its probability: no value is rounded.  The query is brought into float16's range by a power
-//    of two per row, and the weights w_j = p_j scale_j are held against their own running maximum, so that
-//    float16 (2^-11) holds them whatever the scales are.  Subtracting zero points and rounding to 16 bits
-//    pair by pair instead took 44 instructions per key and head of 128 and kept the cache's bytes waiting
-//    (64 users, 8 bits: 196 us).
+//    their own running maximum, so that float16 (2^-11) holds them whatever the scales are.  (Converting
+//    pair by pair to 16 bits through fp32: 44 instructions per key and head of 128.)
 //  * The keys of all sequences are one line of 64-key units, cut into equal shares, one per resident
 //    CTA: ragged lengths balance, and one long sequence fills the GPU.  A CTA's share has at most two
 //    unfinished (sequence, head) pieces, its first and its last; those leave (maximum, sum, weighted
 //    sum) behind and a second launch joins them in order, so results do not depend on timing.
+//  * Few items of short contexts go to clusters of CTAs instead, an item each, which join through shared
+//    memory in the same launch (one user, 32 heads, 2500 keys: 16.2 -> 11.7 us; its bytes take 6.4).
 // Each warp walks its own keys with its own running maximum and sum (fp32).
 #include <algorithm>
 #include <type_traits>

@@ -353,6 +353,54 @@ def _masked_reference(c, L, n, bad):
     return R.attention(_np(c["q"][:first]), k[:bad], v[:bad])
 
 
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("rows", [1, 5])
+def test_attention_many_sequences_share_pages(bits, rows):
+    """More sequences than threads of a CTA, of all short lengths, all over the same few pages; a group of 4, so
+    that 5 rows are a chunk."""
+    D, H, P, dtype, S = 64, 2, 16, torch.bfloat16, 700
+    c = _case([130], [1], H, D, P, bits, dtype, 8, Hq=4 * H)
+    k, v = c["vals"][0]
+    g = torch.Generator().manual_seed(3)
+    have = torch.randint(rows, 131, (S,), generator=g).tolist()
+    new = [rows if s % 3 else 1 for s in range(S)]
+    dev = device()
+    c["table"] = c["table"].expand(S, -1).contiguous()
+    c["lens"] = torch.tensor(have, dtype=torch.int32).to(dev)
+    c["starts"] = torch.tensor([0] + new).cumsum(0).int().to(dev)
+    c["q"] = _randn((sum(new), 4 * H, D), 9, dtype).to(dev)
+    out, at = _np(_attend(c, bits, max_q_len=rows)), 0
+    for s in range(S):
+        if s < 40 or s % 29 == 0 or s > S - 20:
+            ref, mass, size = R.attention(_np(c["q"][at:at + new[s]]), k[:have[s]], v[:have[s]])
+            assert np.all(np.abs(out[at:at + new[s]] - ref) <= _bound(ref, mass, size, dtype, bits, D)), s
+        at += new[s]
+    assert np.isfinite(out).all() and gq.device_status() == 0
+
+
+def test_attention_of_two_threads_at_once():
+    """Calls from two host threads, each on its own stream, give the bits of calls one after another."""
+    import threading
+
+    cases = [_case([300, 513, 64], [300, 100, 1], 2, 128, 32, b, torch.bfloat16, 30 + b, Hq=8) for b in (16, 8)]
+    want = [_attend(c, b) for c, b in zip(cases, (16, 8))]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[i] = [_attend(cases[i], (16, 8)[i]) for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20 and all(torch.equal(o, want[i]) for o in got[i])
+
+
 def test_attention_padding_rows_and_empty():
     D, bits = 64, 8
     c = _case([50, 30], [2, 1], 2, D, 16, bits, torch.bfloat16, 5, pad_rows=4, Hq=4)

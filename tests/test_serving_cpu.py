@@ -81,18 +81,18 @@ def test_cache_read_rejections(L, kw, status):
 def _attend(L, **kw):
     a = dict(q=FAKE, dtype=2, tokens=4, q_heads=8, heads=2, d=128, qt=1024, qh=128, kc=FAKE, vc=FAKE, ks=FAKE, kz=FAKE,
              vs=FAKE, vz=FAKE, bits=8, pages=4, page=64, table=FAKE, width=4, lens=FAKE, starts=FAKE, seqs=2, max_q=4,
-             causal=1, scale=0.1, out=FAKE, stream=None)
+             causal=1, scale=0.1, out=2 * FAKE, stream=None)
     a.update(kw)
     return L.gptq_paged_attention(*a.values())
 
 
 @pytest.mark.parametrize("kw,status", CACHE + [
-    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(out=FAKE), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
     (dict(starts=None), INVALID), (dict(tokens=-1), INVALID), (dict(seqs=-1), INVALID), (dict(q_heads=0), INVALID),
     (dict(q_heads=9), INVALID), (dict(width=0), INVALID), (dict(max_q=-1), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
     (dict(q_heads=130), UNSUPPORTED), (dict(qt=1025), UNSUPPORTED), (dict(q=ODD), UNSUPPORTED), (dict(out=ODD), UNSUPPORTED),
-    (dict(seqs=1 << 21), UNSUPPORTED), (dict(tokens=0), OK), (dict(seqs=0, table=None, lens=None), OK), (dict(max_q=0), OK)])
+    (dict(seqs=1 << 21), UNSUPPORTED), (dict(width=1 << 25), UNSUPPORTED), (dict(width=1 << 28), UNSUPPORTED), (dict(tokens=0), OK), (dict(seqs=0, table=None, lens=None), OK), (dict(max_q=0), OK)])
 def test_attention_rejections(L, kw, status):
     assert _attend(L, **kw) == status
 
