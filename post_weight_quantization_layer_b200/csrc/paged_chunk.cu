@@ -25,8 +25,9 @@
 // tensor core twice and 1024 cycles of the 16-per-cycle exponential unit.  A half's turn takes about 2000 cycles
 // of softmax and 850 of waiting for its products, and two halves share the tensor core: 1.15-1.24 PFLOP/s over a
 // long 16-bit cache (1024 new tokens, 64 heads over 8, 16384 keys: 430-460 us; the clock falls to 1.4 GHz).
-// Codes cost the converters' instructions and shared-memory traffic beside the tensor core's own: 650 us in 8
-// bits, 710 in 4.  Short prompts pay for each tile's start and end (four of 2048, 32 heads: 200-215 us).
+// Codes cost the converters' instructions and shared-memory traffic beside the tensor core's own: 622 us in 8
+// bits, 710 in 4.  Short prompts pay for each tile's start and end, about 10000 of 33000 cycles (four of 2048, 32
+// heads: 188 us).
 #include <cuda.h>
 
 #include <algorithm>
@@ -860,6 +861,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a warp's copy
       const int c = lane % LPR;
       uint32_t ph = 1u;
+      // from a row to the one RPI rows on: steps of tokens and heads, a wrap of the heads at most (with a division and
+      // products per row the first scores of a tile came 8100 cycles after the last ones' results, instead of 4600)
+      const int dt = RPI / a.group, dg = RPI - dt * a.group;
+      const int64_t step = dt * a.q_ts + dg * a.q_hs, wrap = a.q_ts - a.group * a.q_hs;
       JobReader reader(jobs, b);
       Job job;
       while (ok) {
@@ -873,18 +878,20 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         ph ^= 1u;
         const uint32_t row0 = job.tile * CH_ROWS + w * 128 + lane / LPR;
-        uint32_t i = row0 / static_cast<uint32_t>(a.group), g = row0 - i * a.group;  // token and head of the row
+        const uint32_t i = row0 / static_cast<uint32_t>(a.group);  // token and head of the row
+        int g = row0 - i * a.group;
         const T* base = static_cast<const T*>(a.q) + job.start * a.q_ts + job.head * a.group * a.q_hs + c * 8;
-#pragma unroll 4
+        const T* src = base + i * a.q_ts + g * a.q_hs;
+#pragma unroll 8
         for (int r = lane / LPR; r < 128; r += RPI) {
-          const T* src = r < rows ? base + i * a.q_ts + g * a.q_hs : base;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(qs + chunk_off(r, c))), "l"(src),
-                       "r"(r < rows ? 16 : 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(qs + chunk_off(r, c))),
+                       "l"(r < rows ? src : base), "r"(r < rows ? 16 : 0)
                        : "memory");
-          g += RPI;
-          while (g >= static_cast<uint32_t>(a.group)) {
+          src += step;
+          g += dg;
+          if (g >= a.group) {
             g -= a.group;
-            ++i;
+            src += wrap;
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");

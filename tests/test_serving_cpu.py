@@ -1,5 +1,5 @@
-"""Refusals of the serving operators (C ABI and Python binding) and the rotary frequencies (host
-code), without a GPU.  Only calls that are rejected, or that have no work, reach the library:
+"""Refusals of the serving operators (C ABI and Python binding), the rotary frequencies (host code)
+and pins of the oracle, without a GPU.  Only calls that are rejected, or that have no work, reach the library:
 pointers are fake and never read."""
 
 import ctypes
@@ -134,6 +134,58 @@ def test_oracle_quantizer_keeps_the_nearest_code():
         got = np.abs(x - s[:, None].astype(np.float64) * (c.astype(np.float64) - z[:, None]))
         assert np.all(got <= best + 1e-12 * np.abs(x))
         assert np.array_equal(R.unpack_vector_codes(R.pack_vector_codes(c, bits), bits), c)
+
+
+def test_oracle_quantizer_by_hand():
+    """Worked cases: no value, one sign, both signs with ties, not finite."""
+    x = np.array([[0.0, 0, 0, 0], [15, 0, 7.5, 6.5], [-15, 0, -7.5, -1], [-5, 10, 0.5, 1.5], [math.inf, 1, 2, 3],
+                  [math.nan, 1, 2, 3], [3e38, -3e38, 0, 1]])
+    c, s, z = R.quantize_vectors(x, 4)
+    two = np.float32(2.0) / np.float32(15.0)  # no value: from -1 to 1, the zero near 7.5
+    assert s[0] == two and z[0] == round(1.0 / float(two)) and np.all(c[0] == z[0])
+    assert s[1] == 1 and z[1] == 0 and c[1].tolist() == [15, 0, 8, 6]        # 7.5 -> 8, 6.5 -> 6: half to even
+    assert s[2] == 1 and z[2] == 15 and c[2].tolist() == [0, 15, 7, 14]      # 15 - 8
+    assert s[3] == 1 and z[3] == 5 and c[3].tolist() == [0, 15, 5, 7]        # 0.5 -> 0, 1.5 -> 2
+    assert np.all(np.isnan(s[4:])) and not c[4:].any() and not z[4:].any()   # the last: its range is past float32
+    assert R.pack_vector_codes(c[1:2], 4).tolist() == [[15, 8 | 6 << 4]]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_oracle_rotation(interleaved):
+    """Position 0 changes nothing, lengths stay, products depend on the distance alone, the rest of the head stays;
+    the first pair's angle is the position."""
+    rng = np.random.default_rng(1)
+    f, _ = R.rotary_frequencies(16)
+    x, y = rng.normal(size=(2, 5, 3, 24))
+    pos = np.array([0, 1, 7, 100, 4000])
+    a, b = R.rotary(x, pos, f, 1.0, interleaved), R.rotary(y, pos + 3, f, 1.0, interleaved)
+    assert np.array_equal(a[0], x[0]) and np.array_equal(a[..., 16:], x[..., 16:])
+    assert np.allclose(np.linalg.norm(a, axis=-1), np.linalg.norm(x, axis=-1), rtol=1e-13)
+    a2, b2 = R.rotary(x, pos + 50, f, 1.0, interleaved), R.rotary(y, pos + 53, f, 1.0, interleaved)
+    assert np.allclose((a * b).sum(-1), (a2 * b2).sum(-1), rtol=0, atol=1e-10)
+    e = np.zeros((1, 1, 16))
+    e[..., 0] = 1.0
+    turned = R.rotary(e, [2], f, 1.0, interleaved)[0, 0]
+    assert math.isclose(turned[0], math.cos(2.0)) and math.isclose(turned[1 if interleaved else 8], math.sin(2.0))
+
+
+def test_oracle_attention():
+    """Equal keys: the mean of what each row sees; one key: its value; a chunk at a time is the whole prompt; rows
+    before the sequence's start see nothing."""
+    rng = np.random.default_rng(2)
+    q, v = rng.normal(size=(6, 4, 8)), rng.normal(size=(6, 2, 8))
+    out = R.attention(q, np.ones((6, 2, 8)), v)[0]
+    mean = np.cumsum(v, 0) / np.arange(1, 7)[:, None, None]
+    assert np.allclose(out, np.repeat(mean, 2, 1), atol=1e-13)
+    k = rng.normal(size=(6, 2, 8))
+    whole = R.attention(q, k, v)[0]
+    assert np.allclose(whole[0], np.repeat(v[0], 2, 0), atol=1e-15)
+    parts = [R.attention(q[i:j], k[:j], v[:j])[0] for i, j in ((0, 1), (1, 4), (4, 6))]
+    assert np.allclose(np.concatenate(parts), whole, atol=1e-14)
+    few = R.attention(q, k[:2], v[:2])[0]
+    assert not few[:4].any() and np.allclose(few[4], np.repeat(v[0], 2, 0), atol=1e-15)
+    full = R.attention(q, k, v, causal=False)[0]
+    assert np.allclose(full[5], whole[5], atol=1e-15) and not np.allclose(full[0], whole[0])
 
 
 # ------------------------------------------------------------------ the binding's own checks
