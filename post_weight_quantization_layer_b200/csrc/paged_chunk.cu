@@ -112,11 +112,28 @@ __device__ __forceinline__ void enter_tile(const Args& a, Piece& p, int u0) {
   p.u1 = static_cast<int>(min(static_cast<int64_t>(t.units), u0 + (p.end - p.at)));
 }
 
-// The first piece of share `cta`; false where it is empty.  All threads; shared: 3 + THREADS / 32 words.
+// The first piece of share `cta`; false where it is empty.  All threads; shared: 3 + THREADS / 32 * 9 words.
 template <int THREADS>
 __device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& p, int64_t& per, int64_t* shared) {
   int64_t all = 0, total;
-  for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += head_units(a, x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int WARPS = THREADS / 32;
+  int64_t* sums = shared + 3 + WARPS;
+  const bool few = a.seqs <= 8 * WARPS;  // a warp per sequence, a lane per tile; otherwise a thread per sequence
+  if (few) {
+    for (int x = warp; x < a.seqs; x += WARPS) {
+      const Seq q = sequence(a, x);
+      const int n = tiles_of(a, q);
+      int64_t u = 0;
+      for (int i = lane; i < n; i += 32) u += tile_of(a, q, i).units;
+      for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      if (lane == 0) sums[x] = u;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.seqs) all = sums[threadIdx.x];
+  } else {
+    for (int x = threadIdx.x; x < a.seqs; x += THREADS) all += head_units(a, x);
+  }
   const int64_t upto = block_scan<THREADS>(all, total, shared + 3) * a.kv_heads;
   total *= a.kv_heads;
   per = share_of(sh, total);
@@ -150,12 +167,23 @@ __device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& 
   p.tiles = tiles_of(a, p.q);
   p.head = static_cast<int>(shared[1] / shared[2]);
   int64_t rem = shared[1] % shared[2];
-  p.tile = 0;
-  for (;;) {
-    const int u = tile_of(a, p.q, p.tile).units;
-    if (rem < u) break;
-    rem -= u;
-    ++p.tile;
+  // the tile that holds unit `rem` of the head: every warp finds it, 32 tiles at a time
+  for (p.tile = 0;; p.tile += 32) {
+    const int mine = p.tile + lane < p.tiles ? tile_of(a, p.q, p.tile + lane).units : 0;
+    int upto32 = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto32, o);
+      if (lane >= o) upto32 += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, rem < upto32);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      p.tile += l;
+      rem -= __shfl_sync(0xffffffffu, upto32 - mine, l);
+      break;
+    }
+    if (p.tile + 32 >= p.tiles) break;  // (does not happen: the head's units are the tiles')
+    rem -= __shfl_sync(0xffffffffu, upto32, 31);
   }
   enter_tile(a, p, static_cast<int>(rem));
   return true;
@@ -453,21 +481,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Piece p;
-  int64_t per;
   next_may_start();
-  // (the operand ring is not in use yet)
-  const bool any = chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem));
-  if (threadIdx.x == 0) {
-    cut[blockIdx.x] = any ? cut_at(p.at, per, p.u0, p.units, p.q, p.head, p.tile) : Cut{0, -1};
-    if (!any) odd[blockIdx.x] = 0;
-  }
-  if (!any) {
-    wait_for_last();
-    return;
-  }
-  const int64_t first = p.at;
-
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
   Bars b;
   b.full = bars;
@@ -515,9 +529,24 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     tmem_alloc(slot, 512);
     tmem_relinquish();
   }
+  Piece p;
+  int64_t per;
+  // (the operand ring is not in use yet)
+  const bool any = chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem));
+  if (threadIdx.x == 0) {
+    cut[blockIdx.x] = any ? cut_at(p.at, per, p.u0, p.units, p.q, p.head, p.tile) : Cut{0, -1};
+    if (!any) odd[blockIdx.x] = 0;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!any) {
+    if (warp == 8) tmem_dealloc(*slot, 512);
+    wait_for_last();
+    return;
+  }
+  const int64_t first = p.at;
+
   const uint32_t tmem = *slot;
   bool ok = true;
 
