@@ -24,9 +24,9 @@
 // Bound by the exponentials and the tensor core together: 128 x 128 scores take 512 cycles of the
 // tensor core twice and 1024 cycles of the 16-per-cycle exponential unit.  A half's turn takes about 2000 cycles
 // of softmax and 850 of waiting for its products, and two halves share the tensor core: 1.15-1.24 PFLOP/s over a
-// long 16-bit cache (1024 new tokens, 64 heads over 8, 16384 keys: 430-460 us; the clock falls to 1.4 GHz).
-// Codes cost the converters' instructions and shared-memory traffic beside the tensor core's own: 622 us in 8
-// bits, 710 in 4.  Short prompts pay for each tile's start and end, about 10000 of 33000 cycles (four of 2048, 32
+// long 16-bit cache (1024 new tokens, 64 heads over 8, 16384 keys: 436-450 us; the clock falls to 1.4 GHz).
+// Codes cost the converters' instructions and shared-memory traffic beside the tensor core's own: 616 us in 8
+// bits, 710 in 4.  Short prompts pay for each tile's start and end, about 9500 of 37000 cycles (four of 2048, 32
 // heads: 188 us).
 #include <cuda.h>
 
