@@ -164,9 +164,10 @@ __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// The shared memory of the CTAs of a cluster.
+// The shared memory of the CTAs of a cluster.  Threads of a warp come here from loops that some of them leave
+// earlier (heads of 64 and an odd number of rows), so the barrier is the form that asks no convergence of them.
 __device__ __forceinline__ void team_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t peer(uint32_t at, int rank) {
   uint32_t r;
