@@ -13,10 +13,12 @@
 //    only) turn codes into 16-bit operands.  Registers move to the softmax.
 //  * 16-bit pages come by TMA straight into the swizzled operand tiles.  Pages of codes come by bulk
 //    copies (codes, scales and zeros of a page and head are contiguous) into a staging ring, from
-//    which the converters write operand tiles, each value rounded once: values to q's type (as cache_read
-//    gives them), keys to float16, with the queries of a bfloat16 call, since the scores' error is what the
-//    rounding of keys makes of it (16384 keys of 8 bits, outputs off by 0.0028 of their size instead of 0.0044).
-//    What does not fit float16 becomes infinite and is found by the second look.
+//    which the converters write operand tiles.  Keys are multiplied as code - zero, at most 8 bits and a sign and
+//    so exact in q's type, and their scales multiply the scores in fp32: neither keys nor queries are rounded,
+//    whatever their size.  (Keys multiplied out and rounded to float16, and bfloat16 queries with them, cost 9 %
+//    less over a long cache, and gave scores of -infinity, unnoticed, where 65504 was exceeded.)  Values are
+//    rounded once to q's type, as cache_read gives them; one past float16's range becomes infinite, makes its rows
+//    infinite or NaN, and is found by the second look.
 //  * The running maximum moves only when it grows by more than 8 (base 2): until then probabilities
 //    reach 2^8 at most, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
 //  * The (row tile, 128 keys) units of the batch are cut into equal shares, one per SM, as in the
@@ -58,17 +60,23 @@ struct Cfg {
   static constexpr int TILE = CH_KEYS * D * 2;         // bytes of an operand tile
   static constexpr int NST = D == 128 ? 4 : 6;         // operand tiles in the ring
   static constexpr int ROW = D * BITS / 8;
-  // staging of codes, scales and zeros, half a tile of keys each
-  static constexpr int RAW = BITS == 16 ? 0 : ((CH_RAW * (ROW + 5) + 127) / 128) * 128;
+  // staging, half a tile of keys each: codes and zeros of keys, codes, scales and zeros of values
+  static constexpr int RAWK = BITS == 16 ? 0 : CH_RAW * (ROW + 1);
+  static constexpr int RAWV = BITS == 16 ? 0 : CH_RAW * (ROW + 5);
   static constexpr int NRAW = BITS == 16 ? 1 : 4;      // two halves of keys, two of values
+  // scales of the keys of a tile, for the softmax: a place more than the ring has for operands of keys
+  static constexpr int NSC = BITS == 16 ? 0 : NST / 2 + 1;
   static constexpr int QOFF = 0;
   static constexpr int RING = 2 * TILE;
   static constexpr int ROFF = RING + NST * TILE;
-  static constexpr int BARS = ROFF + NRAW * RAW;
-  static constexpr int NBARS = 2 * NST + 2 * NRAW + 18;
+  static constexpr int SCALES = ROFF + 2 * (RAWK + RAWV);
+  static constexpr int BARS = SCALES + NSC * CH_KEYS * 4;
+  static constexpr int NBARS = 2 * NST + 2 * NRAW + NSC + 18;
   static constexpr int JOBS = BARS + NBARS * 8 + 8;
-  static constexpr int SMEM = JOBS + 2 * 40 + 1024;
+  static constexpr int SMEM = JOBS + 2 * 40;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static_assert(RAWK % 16 == 0 && RAWV % 16 == 0, "bulk copies start on 16 bytes");
+  static constexpr __device__ int raw_off(int slot) { return ROFF + (slot < 2 ? slot * RAWK : 2 * RAWK + (slot - 2) * RAWV); }
 };
 
 // ------------------------------------------------------------------ the line of units
@@ -353,6 +361,23 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
+// Scores of 32 keys times their scales, which are taken before the wait for the scores.
+__device__ __forceinline__ void take_scales(float4 (&s)[8], const float* scales) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = *reinterpret_cast<const float4*>(scales + 4 * e);
+}
+__device__ __forceinline__ void by_scales(float (&x)[32], const float4 (&s)[8]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float2 lo = mul2(make_float2(x[e], x[e + 1]), make_float2(s[e / 4].x, s[e / 4].y));
+    const float2 hi = mul2(make_float2(x[e + 2], x[e + 3]), make_float2(s[e / 4].z, s[e / 4].w));
+    x[e] = lo.x;
+    x[e + 1] = lo.y;
+    x[e + 2] = hi.x;
+    x[e + 3] = hi.y;
+  }
+}
+
 // Scores of keys (from `key`) that the row does not see become -infinity.
 __device__ __forceinline__ void hide(float (&x)[32], int key, int see) {
 #pragma unroll
@@ -373,21 +398,24 @@ __device__ __forceinline__ float highest(const float (&x)[N][32]) {
 
 // Probabilities 2^(score scale + ref) of a row's 128 scores into tensor memory as 16-bit pairs, over the
 // scores: part c of 32 keys takes columns that part c / 2 has left.  x holds the first parts, the others are
-// read again.  Returns the sum; arrives at `most` and `full` as they get there.  All go through the
-// exponential unit: a share of them by polynomial was faster alone (959 cycles instead of 1168 for a warp
-// with three of eight) and slower here (prompts of 2048, 32 heads: 244 us instead of 223), where its
-// registers and issue slots are missed.
-template <typename T, int KEEP>
-__device__ __forceinline__ float weights(float (&x)[KEEP][32], float scale, float ref, uint32_t dst, int key, int see,
-                                         int least, uint64_t* most, uint64_t* full) {
+// read again (and, over codes, multiplied by their keys' scales again).  Returns the sum; arrives at `most` and
+// `full` as they get there.  All go through the exponential unit: a share of them by polynomial was faster alone
+// (959 cycles instead of 1168 for a warp with three of eight) and slower here (prompts of 2048, 32 heads: 244 us
+// instead of 223), where its registers and issue slots are missed.
+template <typename T, int BITS, int KEEP>
+__device__ __forceinline__ float weights(float (&x)[KEEP][32], const float* scales, float scale, float ref, uint32_t dst,
+                                         int key, int see, int least, uint64_t* most, uint64_t* full) {
   const float2 sc2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     float(&v)[32] = x[c % KEEP];
     if (c >= KEEP) {
+      float4 s[8];
+      if constexpr (BITS < 16) take_scales(s, scales + c * 32);
       tmem_ld_wait();
       settled(v);
+      if constexpr (BITS < 16) by_scales(v, s);
       if (key + CH_KEYS > least) hide(v, key + c * 32, see);
     }
     uint32_t r[16];
@@ -418,7 +446,7 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 }
 
 struct Bars {
-  uint64_t *full, *empty, *rfull, *rempty, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull, *odone, *zero, *done;
+  uint64_t *full, *empty, *rfull, *rempty, *scales, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull, *odone, *zero, *done;
 };
 
 // What the other warps have to know of a piece, as the warp that walks the line tells them through shared
@@ -478,8 +506,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   constexpr int SIZE = chunk_part(D);
   constexpr int KEEP = BITS == 16 ? 4 : 2;
   constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0u : 1u;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Of the keys' operands over codes, (code - zero) KEY_STEP: no product of a finite bfloat16 query and a key, and no
+  // sum of them, is past fp32 then.
+  constexpr float KEY_STEP = FMT ? 0x1p-16f : 1.f;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   next_may_start();
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
@@ -488,7 +518,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   b.empty = b.full + C::NST;
   b.rfull = b.empty + C::NST;
   b.rempty = b.rfull + C::NRAW;
-  b.jfull = b.rempty + C::NRAW;
+  b.scales = b.rempty + C::NRAW;
+  b.jfull = b.scales + C::NSC;
   b.jempty = b.jfull + 2;
   b.qfull = b.jempty + 2;
   b.qfree = b.qfull + 2;
@@ -510,6 +541,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       mbar_init(&b.rfull[i], 1);
       mbar_init(&b.rempty[i], 4);
     }
+    for (int i = 0; i < C::NSC; ++i) mbar_init(&b.scales[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.jfull[i], 1);
       mbar_init(&b.jempty[i], 11 + C::CONV / 32);  // softmax, issuing, query and converting warps
@@ -561,9 +593,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     JobReader reader(jobs, b);
     Job job;
+    const float scale = BITS < 16 ? a.scale_log2 * (1.f / KEY_STEP) : a.scale_log2;
+    uint32_t before = 0, told = 0;  // tiles of the pieces before this one, and with it: the place of their scales
     auto next_job = [&]() {  // the next piece whose tile has this half
       do {
         if (!reader.next(job)) ok = false;
+        before = told;
+        told += max(job.tiles, 0);
       } while (job.tiles >= 0 && job.tile * CH_ROWS + w * 128 >= job.n * a.group);
       return job.tiles >= 0;
     };
@@ -589,18 +625,38 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           break;
         }
         sph ^= 1u;
+        const float* scales = nullptr;
+        if constexpr (BITS < 16) {
+          // (the scores are there, so the scales of all earlier tiles have come)
+          const uint32_t at = before + j, turn = at / C::NSC;
+          if (!mbar_wait(&b.scales[at - turn * C::NSC], turn & 1u, CH_WAIT)) {
+            ok = false;
+            break;
+          }
+          scales = reinterpret_cast<const float*>(smem + C::SCALES) + (at - turn * C::NSC) * CH_KEYS;
+        }
         tc_fence_after();
         // The maximum first, then the probabilities: only KEEP of the four 32-key parts of the scores stay in
         // registers between the two, the others are read from tensor memory again.
         float x[KEEP][32];
         float top = -INFINITY;
-#pragma unroll
+        // (Two turns of one loop over codes: unrolled as well, the converters and the softmax miss the instruction
+        // cache more, 691 us instead of 673 for the long chunk of 8 bits, 346 instead of 319 for prompts.)
+#pragma unroll 1
         for (int c = 4 - KEEP; c >= 0; c -= KEEP) {
 #pragma unroll
           for (int y = 0; y < KEEP; ++y) tmem_ld_x32_nowait(S + (c + y) * 32, x[y]);
+          float4 s[8];
+          if constexpr (BITS < 16) take_scales(s, scales + c * 32);
           tmem_ld_wait();
 #pragma unroll
-          for (int y = 0; y < KEEP; ++y) settled(x[y]);
+          for (int y = 0; y < KEEP; ++y) {
+            settled(x[y]);
+            if constexpr (BITS < 16) {
+              if (y) take_scales(s, scales + (c + y) * 32);
+              by_scales(x[y], s);
+            }
+          }
           if (key + CH_KEYS > least) {
 #pragma unroll
             for (int y = 0; y < KEEP; ++y) hide(x[y], key + (c + y) * 32, see);
@@ -609,10 +665,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         if (j == 0) {
           m = top;
-        } else if (__any_sync(0xffffffffu, (top - m) * a.scale_log2 > CH_GROW)) {
+        } else if (__any_sync(0xffffffffu, (top - m) * scale > CH_GROW)) {
           // all earlier products are complete: they precede these scores on the tensor core
           const float now = fmaxf(m, top);
-          const float f = now == -INFINITY ? 1.f : ex2((m - now) * a.scale_log2);
+          const float f = now == -INFINITY ? 1.f : ex2((m - now) * scale);
           m = now;
           l *= f;
 #pragma unroll
@@ -624,8 +680,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             tmem_st_x16(O + c * 16, r);
           }
         }
-        const float ref = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        l += weights<T, KEEP>(x, a.scale_log2, ref, S, key, see, least, &b.pmost[w], &b.pfull[w]);
+        const float ref = m == -INFINITY ? 0.f : -m * scale;
+        l += weights<T, BITS, KEEP>(x, scales, scale, ref, S, key, see, least, &b.pmost[w], &b.pfull[w]);
       }
       if (!ok) break;
       if (tiles) {
@@ -671,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       }
       const bool fine = odd2.x + odd2.y == 0.f;
       if (mine) {
-        mine[D * CH_ROWS] = m == -INFINITY ? m : m * a.scale_log2;
+        mine[D * CH_ROWS] = m == -INFINITY ? m : m * scale;
         mine[(D + 1) * CH_ROWS] = l;
       }
       tc_fence_before();
@@ -683,7 +739,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       // -------------------------------------------------------------- issue of the matrix products
       // The whole warp walks the loops and one elected lane issues: descriptors then stay in uniform
       // registers (a product issues every 66 cycles; from a single lane's branch every 82, measured alone).
-      constexpr uint32_t iqk = instr_desc(BITS == 16 ? FMT : 0u, false, false, 128, CH_KEYS);
+      constexpr uint32_t iqk = instr_desc(FMT, false, false, 128, CH_KEYS);
       constexpr uint32_t ipv = instr_desc(FMT, false, true, 128, D);
       const bool lead = elect_one();
       Ring<C::NST> ring;
@@ -779,6 +835,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       const int box = min(1 << a.page_shift, BITS == 16 ? CH_KEYS : CH_RAW), boxes = CH_KEYS / box;
       int ji = 0;
       uint32_t jph = 1u;
+      // The scales of a tile's keys come with the first half of its values.  That waits for the values before to be
+      // converted, whose operands have the place of values NST / 2 tiles back: the softmax is past that tile, and so past
+      // the last user of the scales' place.
+      Ring<C::NSC ? C::NSC : 1> keyed;
+      int scaled = 0;
       auto tell = [&](const Job& job) {
         if (!mbar_wait(&b.jempty[ji], jph, CH_WAIT)) return false;
         if (lane == 0) {
@@ -848,16 +909,25 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                   ok = false;
                   break;
                 }
-                uint8_t* dst = smem + C::ROFF + raw.i * C::RAW;
+                if (kv == 1 && hf == 0) {
+                  if (lane == 0) mbar_arrive_expect_tx(&b.scales[keyed.i], static_cast<uint32_t>(n * box * 4));
+                  __syncwarp();
+                  if (lane < n)
+                    bulk_load(smem + C::SCALES + (keyed.i * CH_KEYS + lane * box) * 4, a.ks + at, box * 4, &b.scales[keyed.i]);
+                  ++scaled;
+                  keyed.step();
+                }
+                uint8_t* dst = smem + C::raw_off(raw.i);
                 const int b0 = hf * (boxes / 2), nb = max(0, min(boxes / 2, n - b0));
-                if (lane == 0) mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(nb * box * (C::ROW + 5)));
+                if (lane == 0)
+                  mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(nb * box * (C::ROW + (kv ? 5 : 1))));
                 __syncwarp();
                 if (lane >= b0 && lane < b0 + nb) {
                   const int x = (lane - b0) * box;
                   const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.vc : a.kc) + at * C::ROW;
                   bulk_load(dst + x * C::ROW, codes, box * C::ROW, &b.rfull[raw.i]);
-                  bulk_load(dst + CH_RAW * C::ROW + x * 4, (kv ? a.vs : a.ks) + at, box * 4, &b.rfull[raw.i]);
-                  bulk_load(dst + CH_RAW * (C::ROW + 4) + x, (kv ? a.vz : a.kz) + at, box, &b.rfull[raw.i]);
+                  bulk_load(dst + CH_RAW * C::ROW + x, (kv ? a.vz : a.kz) + at, box, &b.rfull[raw.i]);
+                  if (kv) bulk_load(dst + CH_RAW * (C::ROW + 1) + x * 4, a.vs + at, box * 4, &b.rfull[raw.i]);
                 }
                 ++issued;
                 raw.step();
@@ -879,6 +949,15 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             ph ^= 1u;
           }
           mbar_wait(BITS == 16 ? &b.full[at] : &b.rfull[at], ph, CH_WAIT);
+        }
+        if constexpr (BITS < 16) {
+          for (int k = 0; k < min(scaled, C::NSC); ++k) {
+            if (--keyed.i < 0) {
+              keyed.i += C::NSC;
+              keyed.ph ^= 1u;
+            }
+            mbar_wait(&b.scales[keyed.i], keyed.ph, CH_WAIT);
+          }
         }
       }
     } else {
@@ -924,17 +1003,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (BITS < 16 && !std::is_same<T, __half>::value) {  // float16, as the keys
-#pragma unroll 4
-          for (int r = lane / LPR; r < 128; r += RPI) {
-            uint4* at = reinterpret_cast<uint4*>(qs + chunk_off(r, c));
-            uint4 v = *at;
-            uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) e[x] = pack2<__half>(__uint_as_float(e[x] << 16), __uint_as_float(e[x] & 0xffff0000u));
-            *at = v;
-          }
-        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.qfull[w]);
@@ -971,7 +1039,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               ok = false;
               break;
             }
-            const uint8_t* src = smem + C::ROFF + rs * C::RAW;
+            const uint8_t* src = smem + C::raw_off(rs);
             uint8_t* dst = tile + hf * CH_RAW * 128;
             const int left = rest - hf * CH_RAW;
             uint32_t wd[N][WORDS];
@@ -983,9 +1051,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                 *reinterpret_cast<uint4*>(wd[x]) = *reinterpret_cast<const uint4*>(src + r * C::ROW + col * 16);
               else
                 *reinterpret_cast<uint2*>(wd[x]) = *reinterpret_cast<const uint2*>(src + r * C::ROW + col * 8);
-              // rows past the last key: zeros
-              sc[x] = r < left ? *reinterpret_cast<const float*>(src + CH_RAW * C::ROW + r * 4) : 0.f;
-              zf[x] = __uint_as_float(0x4B000000u | src[CH_RAW * (C::ROW + 4) + r]);  // 2^23 + zero
+              // values past the last: zeros (keys there: scores that no row sees)
+              sc[x] = KEY_STEP;
+              if (kv) sc[x] = r < left ? *reinterpret_cast<const float*>(src + CH_RAW * (C::ROW + 1) + r * 4) : 0.f;
+              zf[x] = __uint_as_float(0x4B000000u | src[CH_RAW * C::ROW + r]);  // 2^23 + zero
             }
 #pragma unroll
             for (int x = 0; x < N; ++x) {
@@ -1003,8 +1072,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                   f.x = __uint_as_float((v & 15u) | 0x4B000000u);
                   f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
                 }
-                f = mul2(add2(f, z2), s2);
-                out[e] = kv ? pack2<T>(f.x, f.y) : pack2<__half>(f.x, f.y);
+                f = mul2(add2(f, z2), s2);  // the difference is exact
+                out[e] = pack2<T>(f.x, f.y);
               }
               // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
               const int r = r0 + x * STEP;

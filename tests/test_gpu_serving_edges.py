@@ -70,3 +70,53 @@ def test_few_items_share_clusters_with_heads_of_64(bits, group):
     for _ in range(5):
         assert torch.equal(out, _attend(c, bits, max_q_len=3))
     assert gq.device_status() == 0
+
+
+# ------------------------------------------------------------------ values at the ends of the types' ranges
+def _outside(kind, L, n, H, group, D, seed):
+    """Keys [L, H, D], queries [n, H * group, D] (bfloat16) and the scale; scores of ordinary size from operands that
+    are not."""
+    g = torch.Generator().manual_seed(seed)
+    k, q = torch.randn(L, H, D, generator=g), torch.randn(n, H * group, D, generator=g)
+    scale = None
+    if kind == "key_80000":  # a first key that the first row sees alone
+        k[:, :, 0] = 0.0
+        k[0] = 0.0
+        k[0, :, 0] = 80000.0
+        q[..., 0] = -1e-4
+    elif kind == "keys_1e5":  # every key, in one channel
+        k[..., 0] = 1e5 * (1 + 0.1 * torch.rand(L, H, generator=g))
+        q[..., 0] = -1e-3
+    elif kind == "keys_1e5_up":
+        k[..., 0] = 1e5 * (1 + 0.1 * torch.rand(L, H, generator=g))
+        q[..., 0] = 1e-3
+    elif kind == "queries_1e5":
+        k[..., 0] = 1e-4 * torch.rand(L, H, generator=g)
+        q[..., 0] = -1e5
+    elif kind == "queries_1e-7":
+        q *= 1e-7
+        scale = 1e6
+    elif kind == "small_keys":
+        k *= 1e-9
+        q *= 1e9
+    elif kind == "large_keys":
+        k *= 1e9
+        q *= 1e-9
+    return q.bfloat16(), k.bfloat16(), scale
+
+
+KINDS = ["key_80000", "keys_1e5", "keys_1e5_up", "queries_1e5", "queries_1e-7", "small_keys", "large_keys"]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 40, 300])
+@pytest.mark.parametrize("kind", KINDS)
+def test_codes_outside_float16(bits, D, n, kind):
+    """Queries and keys behind codes may have any size that their types have, in a prompt as token by token."""
+    H, group, L, dtype = 1, 4, max(n, 150), torch.bfloat16
+    q, k, scale = _outside(kind, L, n, H, group, D, 5 + D + bits)
+    c = _case([L], [n], H, D, 32, bits, dtype, 5, kv=lambda s, L: (k, _randn((L, H, D), 6, dtype)), Hq=H * group)
+    c["q"] = q.to(device())
+    _check(c, _attend(c, bits, scale=scale), [n], dtype, bits, scale)
+    assert gq.device_status() == 0
