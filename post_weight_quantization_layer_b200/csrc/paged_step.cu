@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
       }
       float up = 1.f, sum = 0.f;
       if constexpr (BITS < 16) {
-        // the row over a power of two, in float16, and its sum
+        // the row over a power of two, its largest in 2^14 .. 2^15 of float16 (elements down to 2^-28 of it keep all
+        // their bits; the sums of 128 products with codes stay below 2^33), and its sum
         float top = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk)
@@ -248,9 +249,9 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
           for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f32(reinterpret_cast<const T*>(&raw[kk])[e])));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = max(__float_as_int(top) >> 23, 1);  // biased exponent; infinity: NaN for the whole row
-        const float down = ex < 255 ? __int_as_float((254 - ex) << 23) : __int_as_float(0x7fc00000);
-        up = __int_as_float(ex << 23) * a.scale_log2;
+        const int ex = max(__float_as_int(top) >> 23, 15);  // biased exponent; infinity: NaN for the whole row
+        const float down = ex < 255 ? __int_as_float((254 + 14 - ex) << 23) : __int_as_float(0x7fc00000);
+        up = __int_as_float((ex - 14) << 23) * a.scale_log2;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
           __half2 w[4];

@@ -5,7 +5,7 @@ Bounds, tighter than those of test_gpu_serving, from the roundings that each ker
 16-bit type, 2^-8 bfloat16, 2^-11 float16; size = largest scale * sum|q||k| over the keys seen; mass = sum p |v|):
 * scores: fp32 sums of exact products, D 2^-24 size.  Few rows over codes: the products are with 1024 + code (64 +
   code of 4 bits), whose sums are off by D 2^-24 (1024 + 255) s sum|q| (s the largest key scale), and a query element is
-  rounded where it is under 2^-14 of its row's largest, by 2^-25 of that.  With d of the scores, probabilities move by
+  rounded where it is under 2^-28 of its row's largest, by 2^-39 of that.  With d of the scores, probabilities move by
   expm1(2 d): their own score's error and the sum's.
 * probabilities: u of the products' type (float16 for few rows over codes, otherwise the call's), 2^-20 for exp2 and
   the fp32 sums.  Float16 has no steps below 2^-24: a weight there is off by 2^-25 of what the type's range leaves
@@ -37,7 +37,7 @@ def _bound(c, s, q, rows, ref, mass, size, dtype, bits, scale=None):
     if few and bits < 16:
         big = np.abs(k).max() / (7.5 if bits == 4 else 127.5)  # the range holds 0: at least half of it is one value's
         ds = ds + scale * (D * 2.0 ** -24 * 1279 * big * np.abs(q).sum(-1)
-                           + 2.0 ** -25 * np.abs(q).max(-1) * np.abs(k).sum(-1).max())
+                           + 2.0 ** -39 * np.abs(q).max(-1) * np.abs(k).sum(-1).max())
     rel = up + (0.0 if few or bits == 16 else u) + 2.0 ** -20 + np.expm1(2 * ds)
     flush = 0.0
     if up == 2.0 ** -11:
@@ -102,10 +102,14 @@ def _outside(kind, L, n, H, group, D, seed):
     elif kind == "large_keys":
         k *= 1e9
         q *= 1e-9
+    elif kind == "queries_2^127":
+        k *= 2.0 ** -124
+        q[..., 0] = 1.5 * 2.0 ** 127
+        q[..., 1:] *= 2.0 ** 120
     return q.bfloat16(), k.bfloat16(), scale
 
 
-KINDS = ["key_80000", "keys_1e5", "keys_1e5_up", "queries_1e5", "queries_1e-7", "small_keys", "large_keys"]
+KINDS = ["key_80000", "keys_1e5", "keys_1e5_up", "queries_1e5", "queries_1e-7", "small_keys", "large_keys", "queries_2^127"]
 
 
 @pytest.mark.parametrize("bits", [8, 4])
