@@ -421,8 +421,8 @@ int gptq_cache_read(const void* k_cache, const void* v_cache, const float* k_sca
  * position L - n + i and sees the keys 0 .. position (causal != 0) or 0 .. L-1; head h reads
  * kv head h / (heads / kv_heads):
  *   out = sum_j softmax_j(scale * q . k_j) v_j, softmax over the keys that are seen.
- * A row that sees no key is written as zeros; rows of no sequence are left as they were; out must
- * not overlap q.  Sequences may share pages.  What
+ * A row that sees no key is written as zeros, as is one all of whose scores are -infinity; rows of
+ * no sequence are left as they were; out must not overlap q.  Sequences may share pages.  What
  * lies in keys that a row does not see, NaN or infinity included, does not reach it.  Keys behind
  * 8- and 4-bit codes are multiplied as they are, values may be rounded once to `dtype` first
  * (sequences of many rows).  The waits of the kernel for many rows are bounded: an

@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
           for (int e = 0; e < 4; ++e) {
             const int c = e & 1;
             const bool sees = all || k + kk * 16 + 8 * (e >> 1) + g < see[r][c];
-            p[e] = sees ? ex2(sc[kk][r][e] - m[r][c]) : 0.f;
+            const float top = m[r][c] == -INFINITY ? 0.f : m[r][c];  // scores of -infinity alone so far: weights of 0
+            p[e] = sees ? ex2(sc[kk][r][e] - top) : 0.f;
             l[r][c] += p[e];
             if constexpr (BITS < 16) {
               const float ref = mw[r][c] == -INFINITY ? 0.f : mw[r][c];  // scales of zero alone so far

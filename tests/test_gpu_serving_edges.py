@@ -124,3 +124,27 @@ def test_codes_outside_float16(bits, D, n, kind):
     c["q"] = q.to(device())
     _check(c, _attend(c, bits, scale=scale), [n], dtype, bits, scale)
     assert gq.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("first", [16, 64, 200])
+@pytest.mark.parametrize("have,n", [(300, 1), (300, 4), (5000, 3), (300, 90)])
+def test_scores_of_minus_infinity(dtype, first, have, n):
+    """Keys whose scores are -infinity weigh nothing, wherever they lie: the rest is the answer; a row with no other
+    key is zeros."""
+    D, bits, group = 64, 16, 4
+
+    def kv(s, L):
+        k, v = _randn((L, 1, D), 1, dtype), _randn((L, 1, D), 2, dtype)
+        k[:first, 0, 3] = -float("inf")
+        return k, v
+
+    c = _case([have], [n], 1, D, 16, bits, dtype, 4, kv=kv, Hq=group)
+    c["q"][:, :, 3] = c["q"][:, :, 3].abs() + 0.25
+    out = _attend(c, bits)
+    k, v = c["vals"][0]
+    c["vals"][0] = (k[first:], v[first:])
+    _check(c, out, [n], dtype, bits)
+    c = _case([first], [min(n, first)], 1, D, 16, bits, dtype, 4, kv=kv, Hq=group)
+    c["q"][:, :, 3] = c["q"][:, :, 3].abs() + 0.25
+    assert not _attend(c, bits).any()
