@@ -509,6 +509,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   // Of the keys' operands over codes, (code - zero) KEY_STEP: no product of a finite bfloat16 query and a key, and no
   // sum of them, is past fp32 then.
   constexpr float KEY_STEP = FMT ? 0x1p-16f : 1.f;
+  // Weights in float16 are held against 2^7 (with CH_GROW, up to 2^15): many keys that weigh under 2^-25 of the
+  // largest, float16's last step, may count for something together.
+  constexpr float UP = FMT ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   next_may_start();
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             tmem_st_x16(O + c * 16, r);
           }
         }
-        const float ref = m == -INFINITY ? 0.f : -m * scale;
+        const float ref = m == -INFINITY ? 0.f : UP - m * scale;
         l += weights<T, BITS, KEEP>(x, scales, scale, ref, S, key, see, least, &b.pmost[w], &b.pfull[w]);
       }
       if (!ok) break;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       }
       const bool fine = odd2.x + odd2.y == 0.f;
       if (mine) {
-        mine[D * CH_ROWS] = m == -INFINITY ? m : m * scale;
+        mine[D * CH_ROWS] = m == -INFINITY ? m : m * scale - UP;
         mine[(D + 1) * CH_ROWS] = l;
       }
       tc_fence_before();

@@ -198,6 +198,9 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
   using Y = Lay<D, BITS, NR>;
   using PT = typename std::conditional<BITS == 16, T, __half>::type;  // operands of the products
   constexpr int NK = Y::NK, NO = D / 16;
+  // Weights in float16 are held against 2^15, not 1: many keys that weigh under 2^-25 of the largest, float16's last
+  // step, may count for something together.
+  constexpr float UP = std::is_same<PT, __half>::value ? 15.f : 0.f;
   extern __shared__ __align__(128) uint8_t smem[];  // a ring per warp, then maxima and sums
   float* red_m = reinterpret_cast<float*>(smem + 4 * Y::RING);
   float* red_l = red_m + 4 * 16;
@@ -487,11 +490,11 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
             const int c = e & 1;
             const bool sees = all || k + kk * 16 + 8 * (e >> 1) + g < see[r][c];
             const float top = m[r][c] == -INFINITY ? 0.f : m[r][c];  // scores of -infinity alone so far: weights of 0
-            p[e] = sees ? ex2(sc[kk][r][e] - top) : 0.f;
+            p[e] = sees ? ex2(sc[kk][r][e] - (BITS == 16 ? top - UP : top)) : 0.f;
             l[r][c] += p[e];
             if constexpr (BITS < 16) {
               const float ref = mw[r][c] == -INFINITY ? 0.f : mw[r][c];  // scales of zero alone so far
-              p[e] = sees ? ex2(sc[kk][r][e] + lv[kk][e >> 1] - ref) : 0.f;
+              p[e] = sees ? ex2(sc[kk][r][e] + lv[kk][e >> 1] - (ref - UP)) : 0.f;
             }
           }
           pf[kk][r][0] = turned(pack2<PT>(p[0], p[1]));
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
       for (int c = 0; c < 2; ++c) {
         const int row = 8 * r + 2 * t + c;
         if constexpr (BITS < 16) {  // back to the row's own maximum; upper nibbles came 16 times as large
-          const float f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - m[r][c]);
+          const float f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - UP - m[r][c]);
 #pragma unroll
           for (int i = 0; i < NO; ++i) {
             o[r][i][c] *= f;
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], x);
         if (g == 0) {
-          red_m[warp * 16 + row] = m[r][c];
+          red_m[warp * 16 + row] = BITS == 16 ? m[r][c] - UP : m[r][c];  // what sums and results are held against
           red_l[warp * 16 + row] = l[r][c];
         }
         if (row < rows) {

@@ -38,7 +38,7 @@ def _bound(c, s, q, rows, ref, mass, size, dtype, bits, scale=None):
         big = np.abs(k).max() / (7.5 if bits == 4 else 127.5)  # the range holds 0: at least half of it is one value's
         ds = ds + scale * (D * 2.0 ** -24 * 1279 * big * np.abs(q).sum(-1)
                            + 2.0 ** -39 * np.abs(q).max(-1) * np.abs(k).sum(-1).max())
-    rel = up + (0.0 if few or bits == 16 else u) + 2.0 ** -20 + np.expm1(2 * ds)
+    rel = up + (0.0 if few or bits == 16 else u) + 2.0 ** -20 + np.expm1(np.minimum(2 * ds, 700))
     flush = 0.0
     if up == 2.0 ** -11:
         flush = 2.0 ** (-40 if few else -32) * len(k) * np.abs(v).max()
@@ -148,3 +148,35 @@ def test_scores_of_minus_infinity(dtype, first, have, n):
     c = _case([first], [min(n, first)], 1, D, 16, bits, dtype, 4, kv=kv, Hq=group)
     c["q"][:, :, 3] = c["q"][:, :, 3].abs() + 0.25
     assert not _attend(c, bits).any()
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.float16, 16), (torch.float16, 8), (torch.float16, 4), (torch.bfloat16, 8),
+                                        (torch.bfloat16, 4), (torch.bfloat16, 16)])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_many_small_weights_beside_a_large_one(dtype, bits, n):
+    """A first key that outweighs each of 8191 others by 2^26, and whose value is zero: the others, 2^-13 together, are
+    the answer.  Sequences enough that a CTA meets many keys of one of them."""
+    D, L, H, group, S = 64, 8192, 8, 4, 16
+
+    def kv(s, L):
+        k, v = torch.zeros(L, H, D, dtype=dtype), torch.ones(L, H, D, dtype=dtype)
+        k[0], v[0] = 1.126, 0.0  # score 0.125 * 64 * 2 * 1.126 = 26 ln 2
+        return k, v
+
+    c = _case([L], [n], H, D, 64, bits, dtype, 4, kv=kv, Hq=H * group)
+    dev = device()
+    c["table"] = c["table"].expand(S, -1).contiguous()
+    c["lens"] = torch.full((S,), L, dtype=torch.int32, device=dev)
+    c["starts"] = torch.arange(S + 1, dtype=torch.int32, device=dev) * n
+    c["q"] = torch.full((S * n, H * group, D), 2.0, dtype=dtype, device=dev)
+    out = _attend(c, bits, max_q_len=n)
+    k, v = c["vals"][0]
+    few = n * group <= 16
+    ref = np.empty(n)  # the same of every head and value
+    for i in range(n):
+        score = 0.125 * k[:L - n + i + 1, 0] @ np.full(D, 2.0)
+        w = np.exp(score - score[0])
+        ref[i] = w @ v[:len(w), 0, 0] / w.sum()
+    rel = 2 * U[dtype] + (2.0 ** -11 if few and bits < 16 else U[dtype]) + 2.0 ** -12  # 2^-12: scores of 26, in float32
+    err = np.abs(_np(out).reshape(S, n, -1) - ref[:, None])
+    assert np.all(err <= rel * ref[:, None] + L * 2.0 ** (-40 if few else -32))
