@@ -638,6 +638,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
           scales = reinterpret_cast<const float*>(smem + C::SCALES) + (at - turn * C::NSC) * CH_KEYS;
         }
+        __syncwarp();  // tensor memory is read by whole warps, and a wait ends thread by thread
         tc_fence_after();
         // The maximum first, then the probabilities: only KEEP of the four 32-key parts of the scores stay in
         // registers between the two, the others are read from tensor memory again.
@@ -693,6 +694,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           break;
         }
         oph ^= 1u;
+        __syncwarp();
         tc_fence_after();
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
