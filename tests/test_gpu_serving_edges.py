@@ -20,7 +20,7 @@ import torch
 import post_weight_quantization_layer_b200 as gq
 from oracle import serving_ref as R
 from tests.gpu_util import device
-from tests.test_gpu_serving import U, _attend, _case, _np, _randn
+from tests.test_gpu_serving import CHUNK, GUESS, LATE, STEP, U, _attend, _case, _np, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,8 @@ pytestmark = pytest.mark.gpu
 def _bound(c, s, q, rows, ref, mass, size, dtype, bits, scale=None):
     """Of the rows q [n, heads, D] of sequence s; rows: the sequence's rows of a kv head."""
     k, v = c["vals"][s]
+    if not len(k):
+        return np.zeros_like(ref)  # no keys: zeros
     D = q.shape[-1]
     scale = D ** -0.5 if scale is None else scale
     few = rows <= 16
@@ -180,3 +182,87 @@ def test_many_small_weights_beside_a_large_one(dtype, bits, n):
     rel = 2 * U[dtype] + (2.0 ** -11 if few and bits < 16 else U[dtype]) + 2.0 ** -12  # 2^-12: scores of 26, in float32
     err = np.abs(_np(out).reshape(S, n, -1) - ref[:, None])
     assert np.all(err <= rel * ref[:, None] + L * 2.0 ** (-40 if few else -32))
+
+
+# ------------------------------------------------------------------ the common cases, closer; shapes at the ends
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("H,group,D,P", [(2, 1, 128, 64), (2, 4, 64, 16), (1, 8, 128, 32), (1, 5, 64, 256)])
+@pytest.mark.parametrize("lens", [STEP, GUESS, CHUNK, LATE], ids=["step", "guess", "chunk", "late"])
+def test_attention_within_its_own_roundings(dtype, bits, H, group, D, P, lens):
+    have, new = lens
+    c = _case(have, new, H, D, P, bits, dtype, 70 + D + bits, Hq=H * group)
+    _check(c, _attend(c, bits, max_q_len=max(new)), new, dtype, bits)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("n", [1, 24])
+def test_long_context_within_its_own_roundings(dtype, bits, n):
+    """131072 keys that weigh much the same.  Roundings are many and independent: the 2-norm of the error is held to 4
+    times the quadrature sum of the relative errors' spreads, u / sqrt(3) each of the output, of the probabilities (of
+    the products' type) and of values where many rows meet codes."""
+    D, L, group = 128, 131072, 4
+    g = torch.Generator().manual_seed(bits)
+
+    def kv(s, L):
+        return (0.7 * torch.randn(L, 1, D, generator=g)).to(dtype), torch.randn(L, 1, D, generator=g).to(dtype)
+
+    c = _case([L], [n], 1, D, 128, bits, dtype, 3, kv=kv, Hq=group)
+    out = _np(_attend(c, bits))
+    k, v = c["vals"][0]
+    q = _np(c["q"])
+    ref = np.empty_like(q)
+    for i in range(n):
+        m = L - n + i + 1
+        s = q[i] @ k[:m, 0].T / np.sqrt(D)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        ref[i] = p @ v[:m, 0] / p.sum(-1, keepdims=True)
+    u, few = U[dtype], n * group <= 16
+    up = 2.0 ** -11 if few and bits < 16 else u
+    most = 4 * np.sqrt((u ** 2 + up ** 2 + (0.0 if few or bits == 16 else u) ** 2) / 3)
+    assert np.linalg.norm(out - ref) <= most * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("group,D", [(16, 64), (17, 128), (32, 64), (64, 128), (64, 64)])
+@pytest.mark.parametrize("have,new", [([300, 1, 129], [1, 1, 1]), ([200, 40, 3, 0], [9, 30, 3, 0])],
+                         ids=["tokens", "chunks"])
+def test_groups_to_64(bits, group, D, have, new):
+    """Heads of a kv head up to 64: beyond 16 even single tokens are many rows."""
+    c = _case(have, new, 2, D, 16, bits, torch.bfloat16, 80 + group, Hq=2 * group)
+    _check(c, _attend(c, bits, max_q_len=max(new)), new, torch.bfloat16, bits)
+    assert gq.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("have,new", [([300, 70], [1, 2]), ([300, 70], [200, 33])], ids=["tokens", "chunks"])
+@pytest.mark.parametrize("order", ["heads first", "part of a wider row", "one head for all", "one token for all"])
+def test_queries_of_any_strides(bits, have, new, order):
+    """Queries laid out heads first, with gaps, or repeated (strides of zero)."""
+    H, group, D, dtype = 2, 3, 64, torch.bfloat16
+    c = _case(have, new, H, D, 32, bits, dtype, 90, Hq=H * group)
+    T = sum(new)
+    if order == "heads first":
+        c["q"] = _randn((H * group, T, D), 91, dtype).to(device()).transpose(0, 1)
+    elif order == "part of a wider row":
+        c["q"] = _randn((T + 3, H * group + 2, 2 * D), 91, dtype).to(device())[3:, 1:-1, D:]
+    elif order == "one head for all":
+        c["q"] = _randn((T, 1, D), 91, dtype).to(device()).expand(T, H * group, D)
+    else:
+        c["q"] = _randn((1, H * group, D), 91, dtype).to(device()).expand(T, H * group, D)
+    _check(c, _attend(c, bits, max_q_len=max(new)), new, dtype, bits)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("lens", [STEP, GUESS, CHUNK], ids=["step", "guess", "chunk"])
+def test_attention_gives_the_same_bits_again(dtype, bits, lens):
+    """Every form, with other work and other contents of the workspace between."""
+    have, new = lens
+    c = _case(have, new, 2, 64, 32, bits, dtype, 95, Hq=6)
+    other = _case([900, 20], [700, 20], 2, 128, 16, bits, dtype, 96, Hq=8)
+    want = _attend(c, bits, max_q_len=max(new))
+    for _ in range(4):
+        _attend(other, bits)
+        assert torch.equal(want, _attend(c, bits, max_q_len=max(new)))
