@@ -37,6 +37,14 @@ bool plain(const Tensor* t, at::ScalarType type, int dev, c10::IntArrayRef shape
 }
 int64_t stride(const Tensor* t, int d) { return t->size(d) > 1 ? t->stride(d) : 0; }
 
+// A small whole number; false for anything else, without an exception.
+bool whole(PyObject* o, long* v) {
+  if (!PyLong_Check(o)) return false;
+  int past = 0;
+  *v = PyLong_AsLongAndOverflow(o, &past);
+  return past == 0;
+}
+
 struct Cache {
   void *k, *v;
   float *ks, *vs;
@@ -125,7 +133,8 @@ PyObject* rotary(PyObject*, PyObject* const* o, Py_ssize_t n) {
 // cache_write(k, v, cache's six, slots, bits) -> True
 PyObject* cache_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
   GUARD_BEGIN
-  if (n != 10 || !p_write || !PyLong_Check(o[9])) return none();
+  long bits;
+  if (n != 10 || !p_write || !whole(o[9], &bits)) return none();
   const Tensor *k = tensor(o[0]), *v = tensor(o[1]), *slots = tensor(o[8]);
   if (!k || !k->is_cuda() || code(k->scalar_type()) < 0) return none();
   const int dev = k->get_device();
@@ -134,7 +143,6 @@ PyObject* cache_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
     return none();
   Cache c;
   at::ScalarType type;
-  const long bits = PyLong_AsLong(o[9]);
   if (!cache(o + 2, bits, dev, &c, &type) || c.heads != k->size(1) || c.dim != k->size(2) ||
       (bits == 16 && type != k->scalar_type()) || !plain(slots, at::kInt, dev, {k->size(0)}))
     return none();
@@ -150,11 +158,11 @@ PyObject* cache_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
 // cache_read(cache's six, slots, bits, half) -> (k, v)
 PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
   GUARD_BEGIN
-  if (n != 9 || !p_read || !PyLong_Check(o[7])) return none();
+  long bits;
+  if (n != 9 || !p_read || !whole(o[7], &bits)) return none();
   const Tensor* slots = tensor(o[6]);
   if (!slots || !slots->is_cuda() || slots->dim() != 1) return none();
   const int dev = slots->get_device();
-  const long bits = PyLong_AsLong(o[7]);
   const at::ScalarType type = o[8] == Py_True ? at::kHalf : at::kBFloat16;
   Cache c;
   at::ScalarType held;
@@ -175,11 +183,12 @@ PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
 // paged_attention(q, cache's six, table, lens, starts, bits, max_q or None, causal, scale or None) -> out
 PyObject* paged_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
   GUARD_BEGIN
-  if (n != 14 || !p_attention || !PyLong_Check(o[10])) return none();
+  long bits, rows = 0;
+  if (n != 14 || !p_attention || !whole(o[10], &bits) || (o[11] != Py_None && (!whole(o[11], &rows) || rows < 0)))
+    return none();
   const Tensor *q = tensor(o[0]), *table = tensor(o[7]), *lens = tensor(o[8]), *starts = tensor(o[9]);
   if (!q || !q->is_cuda() || code(q->scalar_type()) < 0 || !table || table->dim() != 2) return none();
   const int dev = q->get_device();
-  const long bits = PyLong_AsLong(o[10]);
   Cache c;
   at::ScalarType held;
   if (dev != c10::cuda::current_device() || !heads(q, q->scalar_type(), dev) || !cache(o + 1, bits, dev, &c, &held) ||
@@ -188,15 +197,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const int64_t T = q->size(0), H = q->size(1), S = table->size(0);
   if (!plain(table, at::kInt, dev, table->sizes()) || !plain(lens, at::kInt, dev, {S}) || !plain(starts, at::kInt, dev, {S + 1}))
     return none();
-  int64_t most = T;
-  if (o[11] != Py_None) {
-    if (!PyLong_Check(o[11])) return none();
-    most = PyLong_AsLongLong(o[11]);
-    if (most < 0) {
-      PyErr_Clear();
-      return none();
-    }
-  }
+  const int64_t most = o[11] == Py_None ? T : rows;
   const int causal = PyObject_IsTrue(o[12]);
   const double scale = o[13] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.dim)) : PyFloat_AsDouble(o[13]);
   if (causal < 0 || PyErr_Occurred()) {
