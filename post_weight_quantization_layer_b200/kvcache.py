@@ -292,7 +292,7 @@ def paged_attention(q, cache, page_table, kv_lens, q_starts, bits=16, max_q_len=
         raise ValueError("max_q_len must be a number of rows")
     st = lib().gptq_paged_attention(q.data_ptr(), _DTYPE[q.dtype], T, Hq, H, D, qt, qh, *ptrs, bits, pages, P,
                                     page_table.data_ptr(), width, kv_lens.data_ptr(), q_starts.data_ptr(), S,
-                                    T if max_q_len is None else max_q_len, 1 if causal else 0,
+                                    T if max_q_len is None else min(max_q_len, T), 1 if causal else 0,
                                     D ** -0.5 if scale is None else scale, out.data_ptr(), _raw_stream(stream, dev))
     _check(st, "gptq_paged_attention")
     return out

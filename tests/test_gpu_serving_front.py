@@ -30,3 +30,14 @@ def test_bits_of_any_size_are_refused_as_such(bits):
                  lambda: gq.paged_attention(q, cache, *ints, bits=bits)):
         with pytest.raises(ValueError, match="bits must be"):
             call()
+
+
+def test_max_q_len_of_any_size():
+    cache, kv, slots, q, ints = _call()
+    want = gq.paged_attention(q, cache, *ints, bits=8)
+    for most in (3, 40, 2 ** 62, 2 ** 63, 2 ** 64, 2 ** 80):
+        assert torch.equal(gq.paged_attention(q, cache, *ints, bits=8, max_q_len=most), want)
+        assert torch.equal(gq.paged_attention(q, cache, *ints, bits=8, max_q_len=most, out=torch.empty_like(q)), want)
+    for most in (-1, -2 ** 64, 1.5):
+        with pytest.raises(ValueError, match="max_q_len"):
+            gq.paged_attention(q, cache, *ints, bits=8, max_q_len=most)
