@@ -87,6 +87,18 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
   return r;
 }
 
+// The library's calls (an allocation from its pool, up to four launches) run without the interpreter's lock, as
+// calls through ctypes do: threads that serve at once do not take turns.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F, typename... A>
+int unlocked(F* f, A... a) {
+  Unlocked u;
+  return f(a...);
+}
+
 #define GUARD_BEGIN try {
 #define GUARD_END                                     \
   }                                                   \
@@ -114,9 +126,9 @@ PyObject* rotary(PyObject*, PyObject* const* o, Py_ssize_t n) {
   }
   Tensor qo = at::empty({T, H, D}, q->options()), ko;
   if (k) ko = at::empty({T, HK, D}, q->options());
-  const int st = p_rotary(q->data_ptr(), k ? k->data_ptr() : nullptr, code(q->scalar_type()), T, static_cast<int>(H),
-                          static_cast<int>(HK), static_cast<int>(D), static_cast<int>(2 * f->size(0)), inter, stride(q, 0),
-                          stride(q, 1), k ? stride(k, 0) : 0, k ? stride(k, 1) : 0,
+  const int st = unlocked(p_rotary, q->data_ptr(), k ? k->data_ptr() : nullptr, code(q->scalar_type()), T,
+                          static_cast<int>(H), static_cast<int>(HK), static_cast<int>(D),
+                          static_cast<int>(2 * f->size(0)), inter, stride(q, 0), stride(q, 1), k ? stride(k, 0) : 0, k ? stride(k, 1) : 0,
                           static_cast<const int32_t*>(pos->data_ptr()), static_cast<const double*>(f->data_ptr()),
                           static_cast<float>(factor), qo.data_ptr(), k ? ko.data_ptr() : nullptr, H * D, D, HK * D, D,
                           stream(dev));
@@ -146,10 +158,10 @@ PyObject* cache_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (!cache(o + 2, bits, dev, &c, &type) || c.heads != k->size(1) || c.dim != k->size(2) ||
       (bits == 16 && type != k->scalar_type()) || !plain(slots, at::kInt, dev, {k->size(0)}))
     return none();
-  const int st = p_write(k->data_ptr(), v->data_ptr(), code(k->scalar_type()), k->size(0), static_cast<int>(c.heads),
-                         static_cast<int>(c.dim), stride(k, 0), stride(k, 1), stride(v, 0), stride(v, 1), c.k, c.v, c.ks,
-                         c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page),
-                         static_cast<const int32_t*>(slots->data_ptr()), stream(dev));
+  const int st = unlocked(p_write, k->data_ptr(), v->data_ptr(), code(k->scalar_type()), k->size(0),
+                          static_cast<int>(c.heads), static_cast<int>(c.dim), stride(k, 0), stride(k, 1), stride(v, 0),
+                          stride(v, 1), c.k, c.v, c.ks, c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page),
+                          static_cast<const int32_t*>(slots->data_ptr()), stream(dev));
   if (st != GPTQ_OK) return PyLong_FromLong(st);
   Py_RETURN_TRUE;
   GUARD_END
@@ -172,9 +184,9 @@ PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const int64_t count = slots->size(0);
   const auto opt = slots->options().dtype(type);
   Tensor k = at::empty({count, c.heads, c.dim}, opt), v = at::empty({count, c.heads, c.dim}, opt);
-  const int st = p_read(c.k, c.v, c.ks, c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page),
-                        static_cast<const int32_t*>(slots->data_ptr()), count, static_cast<int>(c.heads),
-                        static_cast<int>(c.dim), code(type), k.data_ptr(), v.data_ptr(), stream(dev));
+  const int st = unlocked(p_read, c.k, c.v, c.ks, c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page),
+                          static_cast<const int32_t*>(slots->data_ptr()), count, static_cast<int>(c.heads),
+                          static_cast<int>(c.dim), code(type), k.data_ptr(), v.data_ptr(), stream(dev));
   if (st != GPTQ_OK) return PyLong_FromLong(st);
   return pair(k, v);
   GUARD_END
@@ -205,12 +217,12 @@ PyObject* paged_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
     return none();
   }
   Tensor out = at::empty({T, H, c.dim}, q->options());
-  const int st = p_attention(q->data_ptr(), code(q->scalar_type()), T, static_cast<int>(H), static_cast<int>(c.heads),
-                             static_cast<int>(c.dim), stride(q, 0), stride(q, 1), c.k, c.v, c.ks, c.kz, c.vs, c.vz, c.bits,
-                             c.pages, static_cast<int>(c.page), static_cast<const int32_t*>(table->data_ptr()),
-                             table->size(1), static_cast<const int32_t*>(lens->data_ptr()),
-                             static_cast<const int32_t*>(starts->data_ptr()), S, most, causal, static_cast<float>(scale),
-                             out.data_ptr(), stream(dev));
+  const int st = unlocked(p_attention, q->data_ptr(), code(q->scalar_type()), T, static_cast<int>(H),
+                          static_cast<int>(c.heads), static_cast<int>(c.dim), stride(q, 0), stride(q, 1), c.k, c.v, c.ks,
+                          c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page), static_cast<const int32_t*>(table->data_ptr()),
+                          table->size(1), static_cast<const int32_t*>(lens->data_ptr()),
+                          static_cast<const int32_t*>(starts->data_ptr()), S, most, causal, static_cast<float>(scale),
+                          out.data_ptr(), stream(dev));
   if (st != GPTQ_OK) return PyLong_FromLong(st);
   return THPVariable_Wrap(out);
   GUARD_END

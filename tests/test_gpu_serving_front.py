@@ -41,3 +41,52 @@ def test_max_q_len_of_any_size():
     for most in (-1, -2 ** 64, 1.5):
         with pytest.raises(ValueError, match="max_q_len"):
             gq.paged_attention(q, cache, *ints, bits=8, max_q_len=most)
+
+
+SLOW = """
+#include <unistd.h>
+extern "C" {
+int gptq_rotary() { usleep(400000); return 0; }
+int gptq_cache_write() { usleep(400000); return 0; }
+int gptq_cache_read() { usleep(400000); return 0; }
+int gptq_paged_attention() { usleep(400000); return 0; }
+}
+"""
+
+
+def test_threads_call_at_once(tmp_path):
+    """A second copy of the front, on a library whose calls take 0.4 s: those of four threads overlap."""
+    import importlib.util
+    import shutil
+    import subprocess
+    import threading
+    import time
+
+    from post_weight_quantization_layer_b200 import _native
+
+    (tmp_path / "slow.cpp").write_text(SLOW)
+    subprocess.run(["g++", "-shared", "-fPIC", str(tmp_path / "slow.cpp"), "-o", str(tmp_path / "slow.so")], check=True)
+    copy = shutil.copy(_native.BINDING_PATH, tmp_path / "_binding.so")
+    spec = importlib.util.spec_from_file_location("_binding", copy)
+    front = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(front)
+    front.open(str(tmp_path / "slow.so"))
+    cache, kv, slots, q, ints = _call()
+    six = [cache[n] for n in ("k", "v", "k_scales", "k_zeros", "v_scales", "v_zeros")]
+    f, _ = gq.rotary_frequencies(64)
+    calls = [lambda: front.rotary(kv, None, slots, f, 1.0, False), lambda: front.cache_write(kv, kv, *six, slots, 8),
+             lambda: front.cache_read(*six, slots, 8, False),
+             lambda: front.paged_attention(q, *six, *ints, 8, None, True, None)]
+    got = [None] * 4
+
+    def work(i):
+        got[i] = calls[i]()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    start = time.monotonic()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert time.monotonic() - start < 0.9  # one after another: 1.6
+    assert all(r is not None for r in got)
