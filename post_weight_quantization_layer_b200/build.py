@@ -71,7 +71,8 @@ def binding_command(out):
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile every CUDA source into one shared library, and the binding's front; returns the library's
-    path."""
+    path.  Each is put in place as it succeeds: where the front cannot be built, the library is there all the same
+    when this raises."""
     jobs = []
     if force or needs_build():
         jobs.append((LIB, lambda out: [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"),
@@ -81,23 +82,25 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if not jobs:
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
-    running = []
+    running, failed = [], []
     for path, command in jobs:  # side by side
-        cmd = command(path + ".tmp")
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        running.append((path, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
-    failed = []
+        try:
+            cmd = command(path + ".tmp")
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            running.append((path, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+        except (OSError, ImportError, RuntimeError) as e:  # no compiler, no torch
+            failed.append(f"{os.path.basename(path)}: {e}")
     for path, p in running:
         out, err = p.communicate()
         if p.returncode != 0:
             failed.append(f"{os.path.basename(path)}: compiler failed ({p.returncode}):\n{out}\n{err}")
-        elif verbose and (out or err):
+            continue
+        if verbose and (out or err):
             print(out + err, file=sys.stderr)
+        os.replace(path + ".tmp", path)
     if failed:
         raise RuntimeError("\n".join(failed))
-    for path, _ in running:
-        os.replace(path + ".tmp", path)
     return LIB
 
 

@@ -128,7 +128,8 @@ PyObject* rotary(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (k) ko = at::empty({T, HK, D}, q->options());
   const int st = unlocked(p_rotary, q->data_ptr(), k ? k->data_ptr() : nullptr, code(q->scalar_type()), T,
                           static_cast<int>(H), static_cast<int>(HK), static_cast<int>(D),
-                          static_cast<int>(2 * f->size(0)), inter, stride(q, 0), stride(q, 1), k ? stride(k, 0) : 0, k ? stride(k, 1) : 0,
+                          static_cast<int>(2 * f->size(0)), inter, stride(q, 0), stride(q, 1),
+                          k ? stride(k, 0) : 0, k ? stride(k, 1) : 0,
                           static_cast<const int32_t*>(pos->data_ptr()), static_cast<const double*>(f->data_ptr()),
                           static_cast<float>(factor), qo.data_ptr(), k ? ko.data_ptr() : nullptr, H * D, D, HK * D, D,
                           stream(dev));
@@ -219,7 +220,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
   Tensor out = at::empty({T, H, c.dim}, q->options());
   const int st = unlocked(p_attention, q->data_ptr(), code(q->scalar_type()), T, static_cast<int>(H),
                           static_cast<int>(c.heads), static_cast<int>(c.dim), stride(q, 0), stride(q, 1), c.k, c.v, c.ks,
-                          c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page), static_cast<const int32_t*>(table->data_ptr()),
+                          c.kz, c.vs, c.vz, c.bits, c.pages, static_cast<int>(c.page),
+                          static_cast<const int32_t*>(table->data_ptr()),
                           table->size(1), static_cast<const int32_t*>(lens->data_ptr()),
                           static_cast<const int32_t*>(starts->data_ptr()), S, most, causal, static_cast<float>(scale),
                           out.data_ptr(), stream(dev));
