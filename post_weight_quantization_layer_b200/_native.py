@@ -124,7 +124,10 @@ def binding():
             if not os.path.exists(BINDING_PATH):
                 raise RuntimeError(f"native binding missing at {BINDING_PATH}; build it with "
                                    "`python -m post_weight_quantization_layer_b200.build`")
-            import torch  # noqa: F401  (the binding links against its libraries)
+            from .build import binding_abi, built_abi  # imports torch, whose libraries the binding links against
+            if built_abi() != binding_abi():
+                raise RuntimeError(f"the native binding was built for {built_abi()}, this is {binding_abi()}; build it "
+                                   "again with `python -m post_weight_quantization_layer_b200.build`")
             spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)

@@ -20,6 +20,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libgptq.so")
 BINDING = os.path.join(LIBDIR, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_ABI = os.path.join(LIBDIR, "_binding.abi")  # what the binding was built for
 ROOT = os.path.dirname(PKG)
 
 NVCC_FLAGS = [
@@ -50,8 +51,24 @@ def needs_build():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def binding_abi():
+    """What a build of the binding fits: the C++ side of one torch and one Python."""
+    import torch
+
+    return f"torch {torch.__version__} cxx11 {int(torch.compiled_with_cxx11_abi())} {sysconfig.get_config_var('SOABI')}"
+
+
+def built_abi():
+    """The same of the binding that is there; None where that is not known."""
+    try:
+        with open(BINDING_ABI) as f:
+            return f.read().strip()
+    except OSError:
+        return None
+
+
 def binding_needs_build():
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or built_abi() != binding_abi():
         return True
     t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(p) > t for p in [BINDING_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")))
@@ -99,6 +116,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if verbose and (out or err):
             print(out + err, file=sys.stderr)
         os.replace(path + ".tmp", path)
+        if path == BINDING:
+            with open(BINDING_ABI, "w") as f:
+                f.write(binding_abi() + "\n")
     if failed:
         raise RuntimeError("\n".join(failed))
     return LIB

@@ -5,16 +5,40 @@ import os
 import pytest
 
 import post_weight_quantization_layer_b200.build as B
+from post_weight_quantization_layer_b200 import _native
 
 
 @pytest.fixture
 def tree(tmp_path, monkeypatch):
     """A build directory of its own, with a library and a front newer than their sources."""
-    for name, file in (("LIBDIR", ""), ("LIB", "libgptq.so"), ("BINDING", "_binding.so")):
+    for name, file in (("LIBDIR", ""), ("LIB", "libgptq.so"), ("BINDING", "_binding.so"), ("BINDING_ABI", "_binding.abi")):
         monkeypatch.setattr(B, name, str(tmp_path / file))
     (tmp_path / "libgptq.so").write_text("library")
     (tmp_path / "_binding.so").write_text("front")
+    (tmp_path / "_binding.abi").write_text(B.binding_abi() + "\n")
     return tmp_path
+
+
+def test_a_front_for_another_torch_is_built_again_and_not_loaded(tree, monkeypatch):
+    assert not B.needs_build() and not B.binding_needs_build()
+    monkeypatch.setattr(_native, "_binding", None)
+    monkeypatch.setattr(_native, "BINDING_PATH", B.BINDING)
+    for record in ("torch 2.0.0 cxx11 0 cpython-38-x86_64-linux-gnu\n", None):
+        if record is None:
+            os.unlink(B.BINDING_ABI)
+        else:
+            (tree / "_binding.abi").write_text(record)
+        assert B.binding_needs_build() and not B.needs_build()
+        with pytest.raises(RuntimeError, match="was built for"):
+            _native.binding()
+
+
+def test_the_record_follows_a_build(tree, monkeypatch):
+    os.unlink(B.BINDING_ABI)
+    monkeypatch.setattr(B, "binding_command", lambda out: ["sh", "-c", f"echo new > {out}"])
+    assert B.build() == B.LIB
+    assert (tree / "_binding.so").read_text() == "new\n" and (tree / "libgptq.so").read_text() == "library"
+    assert not B.binding_needs_build()
 
 
 @pytest.mark.parametrize("front", [["sh", "-c", "echo no headers >&2; exit 3"], ["no-such-compiler"]])
