@@ -11,6 +11,7 @@ import importlib.util
 import os
 import re
 import threading
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "lib", "libgptq.so")
@@ -136,6 +137,28 @@ def binding():
             module.open(LIB_PATH)
             _binding = module
     return _binding
+
+
+class _NoFront:
+    """Stands where the front cannot be loaded: leaves every call to the wrappers."""
+
+    rotary = cache_write = cache_read = paged_attention = staticmethod(lambda *args: None)
+
+
+_front = None
+
+
+def front():
+    """``binding()`` for the wrappers of the serving operators, which can call the native library without it, some 10
+    us slower: where it cannot be loaded, one warning and a stand-in."""
+    global _front
+    if _front is None:
+        try:
+            _front = binding()
+        except (RuntimeError, ImportError) as e:
+            warnings.warn(f"serving calls go through ctypes: {e}", RuntimeWarning, stacklevel=3)
+            _front = _NoFront
+    return _front
 
 
 def declared_symbols():

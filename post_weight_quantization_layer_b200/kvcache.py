@@ -12,7 +12,7 @@ token, head and side.
 
 The plain case of each call (outputs made here, the current stream) goes through the native front of
 ``csrc/binding.cpp``, which checks, allocates and launches; anything else, and everything that is wrong,
-through the Python below, which says what.
+through the Python below, which says what.  So does every call where the front cannot be loaded (with a warning).
 """
 
 from __future__ import annotations
@@ -22,7 +22,7 @@ import ctypes
 
 import torch
 
-from ._native import binding, lib
+from ._native import front, lib
 from .api import _DTYPE, _check, _need, _need_cuda
 
 SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -157,7 +157,7 @@ def rotary(q, k, positions, inv_freq, attention_factor=1.0, interleaved=False, o
     of a fused projection.  Returns (q, k) as new tensors, or written to out = (q_out, k_out), which
     may be (q, k) themselves."""
     if out is None and stream is None:
-        r = binding().rotary(q, k, positions, inv_freq, attention_factor, interleaved)
+        r = front().rotary(q, k, positions, inv_freq, attention_factor, interleaved)
         if r.__class__ is tuple:
             return r
         if r is not None:
@@ -205,7 +205,7 @@ def cache_write(k, v, cache, slots, bits=16, stream=None):
     below 16 bits.  A slot outside the cache (-1 for a padded token) is left out; the others must
     differ.  Returns the cache."""
     if stream is None:
-        r = binding().cache_write(k, v, *_six(cache, bits), slots, bits)
+        r = front().cache_write(k, v, *_six(cache, bits), slots, bits)
         if r is True:
             return cache
         if r is not None:
@@ -233,7 +233,7 @@ def cache_read(cache, slots, bits=16, dtype=None, stream=None):
     if dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("dtype must be float16 or bfloat16")
     if stream is None:
-        r = binding().cache_read(*_six(cache, bits), slots, bits, dtype is torch.float16)
+        r = front().cache_read(*_six(cache, bits), slots, bits, dtype is torch.float16)
         if r.__class__ is tuple:
             return r
         if r is not None:
@@ -266,7 +266,7 @@ def paged_attention(q, cache, page_table, kv_lens, q_starts, bits=16, max_q_len=
     scale:      of the scores, default head_dim ** -0.5
     Rows that see no key are zeros; rows of no sequence are left as they were in `out`."""
     if out is None and stream is None:
-        r = binding().paged_attention(q, *_six(cache, bits), page_table, kv_lens, q_starts, bits, max_q_len, causal, scale)
+        r = front().paged_attention(q, *_six(cache, bits), page_table, kv_lens, q_starts, bits, max_q_len, causal, scale)
         if isinstance(r, torch.Tensor):
             return r
         if r is not None:

@@ -90,3 +90,22 @@ def test_threads_call_at_once(tmp_path):
         t.join()
     assert time.monotonic() - start < 0.9  # one after another: 1.6
     assert all(r is not None for r in got)
+
+
+def test_the_same_without_the_front(monkeypatch):
+    """Every call through ctypes gives the bits of the native front."""
+    from post_weight_quantization_layer_b200 import _native
+
+    cache, kv, slots, q, ints = _call()
+    pos, (f, a) = slots % 7, gq.rotary_frequencies(64)
+
+    def run():
+        fresh = gq.new_cache(4, 2, 64, 16, 8)
+        gq.cache_write(kv, kv, fresh, slots, 8)
+        return [*gq.rotary(kv, kv[:, :1], pos, f, a), *gq.cache_read(fresh, slots, 8), *fresh.values(),
+                gq.paged_attention(q, fresh, *ints, bits=8)]
+
+    want = run()
+    monkeypatch.setattr(_native, "_front", _native._NoFront)
+    got = run()
+    assert len(want) == len(got) and all(torch.equal(x, y) for x, y in zip(want, got))

@@ -52,3 +52,21 @@ def test_the_library_is_installed_where_the_front_cannot_be_built(tree, monkeypa
     with pytest.raises(RuntimeError, match="_binding.so"):
         B.build()
     assert (tree / "libgptq.so").read_text() == "built\n" and not os.path.exists(B.BINDING)
+
+
+def test_without_the_front_the_wrappers_check_and_call_themselves(tree, monkeypatch):
+    import torch
+
+    import post_weight_quantization_layer_b200 as gq
+
+    for path in (str(tree / "nothing.so"), B.BINDING):  # not there; not a library
+        monkeypatch.setattr(_native, "_binding", None)
+        monkeypatch.setattr(_native, "_front", None)
+        monkeypatch.setattr(_native, "BINDING_PATH", path)
+        kv, slots = torch.zeros(3, 2, 64).bfloat16(), torch.zeros(3, dtype=torch.int32)
+        cache = gq.new_cache(1, 2, 64, 16, 8, device="cpu")
+        with pytest.warns(RuntimeWarning, match="go through ctypes"):
+            with pytest.raises(ValueError, match="CUDA tensors"):
+                gq.cache_write(kv, kv, cache, slots, 8)
+        with pytest.raises(ValueError, match="bits must be"):
+            gq.cache_read(cache, slots, 5)
