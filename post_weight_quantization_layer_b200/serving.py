@@ -40,8 +40,8 @@ def step_batch(pages, have, new, page_size, device=None, width=None) -> StepBatc
         if a < 0 or n < 0 or len(p) * page_size < a + n:
             raise ValueError(f"sequence {s}: {len(p)} pages of {page_size} do not hold {a} + {n} tokens")
     width = max([1, *(len(p) for p in pages)]) if width is None else width
-    if any(len(p) > width for p in pages):
-        raise ValueError("width is less than a sequence's number of pages")
+    if width < 1 or any(len(p) > width for p in pages):
+        raise ValueError("width is less than 1 or than a sequence's number of pages")
     positions, slots, starts = [], [], [0]
     for p, a, n in zip(pages, have, new):
         positions += range(a, a + n)
@@ -75,9 +75,11 @@ class ServedLayer:
 def decoder_layer_step(h, layer: ServedLayer, cache, batch: StepBatch, stream=None, seen=None):
     """New tokens' hidden states h [tokens, hidden] through the layer; the cache (kvcache.new_cache) takes
     their keys and values.  seen: optional dict that receives the intermediate activations.  Returns the
-    layer's output [tokens, hidden]."""
-    stream = stream or torch.cuda.current_stream()
+    layer's output [tokens, hidden]; a step without tokens has none and leaves the cache as it is."""
     T, H, HK = h.shape[0], layer.heads, layer.kv_heads
+    if T == 0:
+        return torch.empty_like(h)
+    stream = stream or torch.cuda.current_stream()
 
     def lin(x, name):
         return api.quantized_linear(x, layer.checkpoints[name], layer.bits, stream=stream)

@@ -70,3 +70,16 @@ def test_without_the_front_the_wrappers_check_and_call_themselves(tree, monkeypa
                 gq.cache_write(kv, kv, cache, slots, 8)
         with pytest.raises(ValueError, match="bits must be"):
             gq.cache_read(cache, slots, 5)
+
+
+def test_a_step_without_tokens():
+    import torch
+
+    from post_weight_quantization_layer_b200 import serving
+
+    batch = serving.step_batch([[3], []], [5, 0], [0, 0], 16, device="cpu")
+    layer = serving.ServedLayer({}, (), 4, 2, torch.zeros(32, dtype=torch.float64))
+    out = serving.decoder_layer_step(torch.zeros(0, 256).bfloat16(), layer, {}, batch)
+    assert out.shape == (0, 256) and out.dtype == torch.bfloat16
+    with pytest.raises(ValueError, match="width"):
+        serving.step_batch([[], []], [0, 0], [0, 0], 16, device="cpu", width=0)
