@@ -49,7 +49,7 @@ constexpr int CH_ROWS = kTileRows;
 constexpr int CH_KEYS = 128;  // keys of a unit
 constexpr int CH_RAW = 64;    // keys of a staging slot
 constexpr uint32_t CH_WAIT = 1u << 22;
-constexpr float CH_GROW = 8.f;
+constexpr float CH_GROW = 8.f;  // an online softmax that rescales only where the maximum grew by more (base 2)
 
 __device__ int g_chunk_status = 0;
 
@@ -122,7 +122,7 @@ __device__ __forceinline__ void enter_tile(const Args& a, Piece& p, int u0) {
 
 // The first piece of share `cta`; false where it is empty.  All threads; shared: 3 + THREADS / 32 * 9 words.
 template <int THREADS>
-__device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& p, int64_t& per, int64_t* shared) {
+__device__ bool chunk_first(const Args& a, int64_t cta, Piece& p, int64_t& per, int64_t* shared) {
   int64_t all = 0, total;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int WARPS = THREADS / 32;
@@ -144,7 +144,9 @@ __device__ bool chunk_first(const Args& a, const Share& sh, int64_t cta, Piece& 
   }
   const int64_t upto = block_scan<THREADS>(all, total, shared + 3) * a.kv_heads;
   total *= a.kv_heads;
-  per = share_of(sh, total);
+  // Few units: a CTA each, since a unit takes longer than its part takes to join (206 tokens of 64 heads over 281
+  // keys: 28 us instead of 43 with 8 units at least and 30 with 4; 64 tokens alone: 20, 60 and 37).
+  per = (total + gridDim.x - 1) / gridDim.x;
   p.at = cta * per;
   p.end = min(total, p.at + per);
   if (p.at >= p.end) return false;
@@ -501,7 +503,7 @@ struct Ring {
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Args a,
-                 const Share sh, float* __restrict__ part, Cut* __restrict__ cut, int* __restrict__ odd) {
+                 float* __restrict__ part, Cut* __restrict__ cut, int* __restrict__ odd) {
   using C = Cfg<D, BITS>;
   constexpr int SIZE = chunk_part(D);
   constexpr int KEEP = BITS == 16 ? 4 : 2;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   Piece p;
   int64_t per;
   // (the operand ring is not in use yet)
-  const bool any = chunk_first<C::THREADS>(a, sh, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem));
+  const bool any = chunk_first<C::THREADS>(a, blockIdx.x, p, per, reinterpret_cast<int64_t*>(smem));
   if (threadIdx.x == 0) {
     cut[blockIdx.x] = any ? cut_at(p.at, per, p.u0, p.units, p.q, p.head, p.tile) : Cut{0, -1};
     if (!any) odd[blockIdx.x] = 0;
@@ -589,7 +591,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     // ---------------------------------------------------------------- softmax, one thread per row
     regs_more<BITS == 16 ? 216 : 136>();
     const int w = warp >> 2, wr = (warp & 3) * 32 + lane;  // half, row of the half
-    uint8_t* qs = smem + C::QOFF + w * C::TILE;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t S = tmem + lanes + w * 128, O = tmem + lanes + 256 + w * D;
     uint32_t sph = 0, oph = 0;
@@ -1194,16 +1195,8 @@ int run(const Args& a, int grid, float* part, Cut* cut, int* odd, bool next, cud
     GPTQ_TRY(cache_map<T>(&tk, a.kc, a, D));
     GPTQ_TRY(cache_map<T>(&tv, a.vc, a, D));
   }
-  Share sh;
-  sh.whole = 0;
-  // Few units: a CTA each, since a unit takes longer than its part takes to join (206 tokens of 64 heads over 281
-  // keys: 28 us instead of 43 with 8 units at least and 30 with 4; 64 tokens alone: 20, 60 and 37).
-  sh.min_per = 1;
-  sh.rows_lo = kStepRows + 1;
-  sh.rows_hi = 0x7fffffff;
-  sh.grid = grid;
-  if (next) return launch_next(chunk_kernel<T, D, BITS>, dim3(grid), C::THREADS, C::SMEM, s, tk, tv, a, sh, part, cut, odd);
-  chunk_kernel<T, D, BITS><<<grid, C::THREADS, C::SMEM, s>>>(tk, tv, a, sh, part, cut, odd);
+  if (next) return launch_next(chunk_kernel<T, D, BITS>, dim3(grid), C::THREADS, C::SMEM, s, tk, tv, a, part, cut, odd);
+  chunk_kernel<T, D, BITS><<<grid, C::THREADS, C::SMEM, s>>>(tk, tv, a, part, cut, odd);
   return after_launch();
 }
 

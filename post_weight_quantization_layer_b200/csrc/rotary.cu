@@ -121,12 +121,13 @@ template <typename T, bool VEC, bool INTER>
 void launch_rotary(const RotaryArgs& a, cudaStream_t s) {
   // Four tokens per CTA share one round of cosines; few tokens: one per CTA, its heads over
   // as many CTAs as fill the SMs.
-  if (a.tokens >= 4 * 148) {
+  const int sms = num_sms();
+  if (a.tokens >= 4 * sms) {
     rotary_kernel<T, VEC, INTER, 4><<<static_cast<unsigned>((a.tokens + 3) / 4), RT_THREADS, 0, s>>>(a);
   } else {
     const int items = (a.heads + a.kv_heads) * std::max(1, a.d / 16);
     const unsigned most = static_cast<unsigned>(std::max(1, items / RT_THREADS));
-    const unsigned want = static_cast<unsigned>(std::max<int64_t>(1, 2 * 148 / a.tokens));
+    const unsigned want = static_cast<unsigned>(std::max<int64_t>(1, 2 * sms / a.tokens));
     rotary_kernel<T, VEC, INTER, 1><<<dim3(static_cast<unsigned>(a.tokens), std::min(most, want)), RT_THREADS, 0, s>>>(a);
   }
 }
