@@ -569,11 +569,12 @@ __global__ void __launch_bounds__(ST_THREADS, (Lay<D, BITS, NR>::CTAS))
       for (int c = 0; c < 2; ++c) {
         const int row = 8 * r + 2 * t + c;
         if constexpr (BITS < 16) {  // back to the row's own maximum; upper nibbles came 16 times as large
-          const float f = mw[r][c] == -INFINITY ? 0.f : ex2(mw[r][c] - UP - m[r][c]);
+          // the factor by its root: of small values it may be below float32's range when the product is not
+          const float f = mw[r][c] == -INFINITY ? 0.f : ex2(0.5f * (mw[r][c] - UP - m[r][c]));
 #pragma unroll
           for (int i = 0; i < NO; ++i) {
-            o[r][i][c] *= f;
-            o[r][i][2 + c] *= BITS == 4 ? f * 0.0625f : f;
+            o[r][i][c] = o[r][i][c] * f * f;
+            o[r][i][2 + c] = o[r][i][2 + c] * (BITS == 4 ? f * 0.0625f : f) * f;
           }
         }
 #pragma unroll

@@ -266,3 +266,15 @@ def test_attention_gives_the_same_bits_again(dtype, bits, lens):
     for _ in range(4):
         _attend(other, bits)
         assert torch.equal(want, _attend(c, bits, max_q_len=max(new)))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("size", [2.0 ** -120, 2.0 ** -60, 1e-7, 1e7, 2.0 ** 100, "mixed"])
+def test_values_behind_codes_of_any_size(bits, n, size):
+    """Values from the smallest to the largest that bfloat16 has, one size or all in one sequence."""
+    D, H, group, L, dtype = 64, 1, 4, max(n, 150), torch.bfloat16
+    v = _randn((L, H, D), 6, torch.float32)
+    v *= torch.logspace(-8, 8, L, base=10.0)[torch.randperm(L)][:, None, None] if size == "mixed" else size
+    c = _case([L], [n], H, D, 16, bits, dtype, 5, kv=lambda s, L: (_randn((L, H, D), 5, dtype), v.to(dtype)), Hq=H * group)
+    _check(c, _attend(c, bits), [n], dtype, bits)
