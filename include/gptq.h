@@ -423,10 +423,9 @@ int gptq_cache_read(const void* k_cache, const void* v_cache, const float* k_sca
  *   out = sum_j softmax_j(scale * q . k_j) v_j, softmax over the keys that are seen.
  * A row that sees no key is written as zeros, as is one all of whose scores are -infinity; rows of
  * no sequence are left as they were; out must not overlap q.  Sequences may share pages.  What
- * lies in keys that a row does not see, NaN or infinity included, does not reach it.  Keys behind
- * 8- and 4-bit codes are multiplied as they are, values may be rounded once to `dtype` first
- * (sequences of many rows).  The waits of the kernel for many rows are bounded: an
- * expiry is GPTQ_ERR_TIMEOUT of gptq_device_status.
+ * lies in keys that a row does not see, NaN or infinity included, does not reach it.  What stands
+ * behind 8- and 4-bit codes is multiplied as it is; the weights are rounded once to 16 bits.  The
+ * waits of the kernel for many rows are bounded: an expiry is GPTQ_ERR_TIMEOUT of gptq_device_status.
  * heads a multiple of kv_heads; heads / kv_heads at most 64; table_width * page_size below 2^31 - 1024.  max_q_len: the most rows of a
  * sequence (longer ones would lose rows), at most `tokens`.  q_starts [seqs + 1] runs upwards
  * inside 0 .. tokens; a length above table_width * page_size is cut to it and a page id

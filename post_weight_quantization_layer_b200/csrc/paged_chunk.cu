@@ -14,11 +14,13 @@
 //  * 16-bit pages come by TMA straight into the swizzled operand tiles.  Pages of codes come by bulk
 //    copies (codes, scales and zeros of a page and head are contiguous) into a staging ring, from
 //    which the converters write operand tiles.  Keys are multiplied as code - zero, at most 8 bits and a sign and
-//    so exact in q's type, and their scales multiply the scores in fp32: neither keys nor queries are rounded,
-//    whatever their size.  (Keys multiplied out and rounded to float16, and bfloat16 queries with them, cost 9 %
-//    less over a long cache, and gave scores of -infinity, unnoticed, where 65504 was exceeded.)  Values are
-//    rounded once to q's type, as cache_read gives them; one past float16's range becomes infinite, makes its rows
-//    infinite or NaN, and is found by the second look.
+//    so exact in q's type, and their scales multiply the scores in fp32; values as (code - zero) times their scale's
+//    power of two, exact too, and the rest of the scale multiplies the probabilities in fp32, before they are rounded.
+//    So nothing behind a code is rounded, nor a query, whatever its size; what remains is the rounding of the weights,
+//    as over a 16-bit cache.  (All multiplied out and rounded, keys and bfloat16 queries to float16, values to q's type,
+//    a long cache of 8 bits took 13 % less time: scores were -infinity, unnoticed, where 65504 was exceeded, and errors
+//    1.7 times those of an answer in fp32 rounded once, now 1.36.)  A float16 call's value past that type's range is
+//    infinite, makes its rows infinite or NaN, and is found by the second look.
 //  * The running maximum moves only when it grows by more than 8 (base 2): until then probabilities
 //    reach 2^8 at most, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
 //  * The (row tile, 128 keys) units of the batch are cut into equal shares, one per SM, as in the
@@ -60,23 +62,22 @@ struct Cfg {
   static constexpr int TILE = CH_KEYS * D * 2;         // bytes of an operand tile
   static constexpr int NST = D == 128 ? 4 : 6;         // operand tiles in the ring
   static constexpr int ROW = D * BITS / 8;
-  // staging, half a tile of keys each: codes and zeros of keys, codes, scales and zeros of values
-  static constexpr int RAWK = BITS == 16 ? 0 : CH_RAW * (ROW + 1);
-  static constexpr int RAWV = BITS == 16 ? 0 : CH_RAW * (ROW + 5);
+  // staging of codes and zeros, half a tile of keys or values each
+  static constexpr int RAW = BITS == 16 ? 0 : CH_RAW * (ROW + 1);
   static constexpr int NRAW = BITS == 16 ? 1 : 4;      // two halves of keys, two of values
-  // scales of the keys of a tile, for the softmax: a place more than the ring has for operands of keys
-  static constexpr int NSC = BITS == 16 ? 0 : NST / 2 + 1;
+  // places for the scales of a tile's keys and values: as many as the ring has for operands of values (one more, and no
+  // wait for a free one, has no room beside 8-bit keys of 128 and gained nothing elsewhere)
+  static constexpr int NSC = BITS == 16 ? 0 : NST / 2;
   static constexpr int QOFF = 0;
   static constexpr int RING = 2 * TILE;
   static constexpr int ROFF = RING + NST * TILE;
-  static constexpr int SCALES = ROFF + 2 * (RAWK + RAWV);
-  static constexpr int BARS = SCALES + NSC * CH_KEYS * 4;
-  static constexpr int NBARS = 2 * NST + 2 * NRAW + NSC + 18;
+  static constexpr int SCALES = ROFF + NRAW * RAW;
+  static constexpr int BARS = SCALES + NSC * 2 * CH_KEYS * 4;
+  static constexpr int NBARS = 2 * NST + 2 * NRAW + 2 * NSC + 18;
   static constexpr int JOBS = BARS + NBARS * 8 + 8;
   static constexpr int SMEM = JOBS + 2 * 40;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  static_assert(RAWK % 16 == 0 && RAWV % 16 == 0, "bulk copies start on 16 bytes");
-  static constexpr __device__ int raw_off(int slot) { return ROFF + (slot < 2 ? slot * RAWK : 2 * RAWK + (slot - 2) * RAWV); }
+  static_assert(RAW % 16 == 0, "bulk copies start on 16 bytes");
 };
 
 // ------------------------------------------------------------------ the line of units
@@ -363,6 +364,17 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
+// A value's scale is a power of two with the sign, by which its codes are multiplied, exactly, times a part of 1 .. 2, by
+// which its weight is.  (Below float32's normal range: the scale, and 1.)
+__device__ __forceinline__ float power_of(float s) {
+  const uint32_t w = __float_as_uint(s);
+  return (w & 0x7f800000u) ? __uint_as_float(w & 0xff800000u) : s;
+}
+__device__ __forceinline__ float part_of(float s) {
+  const uint32_t w = __float_as_uint(s);
+  return (w & 0x7f800000u) ? __uint_as_float((w & 0x007fffffu) | 0x3f800000u) : 1.f;
+}
+
 // Scores of 32 keys times their scales, which are taken before the wait for the scores.
 __device__ __forceinline__ void take_scales(float4 (&s)[8], const float* scales) {
 #pragma unroll
@@ -407,6 +419,7 @@ __device__ __forceinline__ float highest(const float (&x)[N][32]) {
 template <typename T, int BITS, int KEEP>
 __device__ __forceinline__ float weights(float (&x)[KEEP][32], const float* scales, float scale, float ref, uint32_t dst,
                                          int key, int see, int least, uint64_t* most, uint64_t* full) {
+  const float* parts = scales + CH_KEYS;  // of the values' scales
   const float2 sc2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -427,6 +440,7 @@ __device__ __forceinline__ float weights(float (&x)[KEEP][32], const float* scal
       p.x = ex2(p.x);
       p.y = ex2(p.y);
       sum[e & 1] = add2(sum[e & 1], p);
+      if constexpr (BITS < 16) p = mul2(p, *reinterpret_cast<const float2*>(parts + c * 32 + 2 * e));
       r[e] = pack2<T>(p.x, p.y);
     }
     if (c + KEEP < 4) tmem_ld_x32_nowait(dst + (c + KEEP) * 32, v);
@@ -448,7 +462,7 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 }
 
 struct Bars {
-  uint64_t *full, *empty, *rfull, *rempty, *scales, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull, *odone, *zero, *done;
+  uint64_t *full, *empty, *rfull, *rempty, *scales, *parts, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull, *odone, *zero, *done;
 };
 
 // What the other warps have to know of a piece, as the warp that walks the line tells them through shared
@@ -513,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   constexpr float KEY_STEP = FMT ? 0x1p-16f : 1.f;
   // Weights in float16 are held against 2^7 (with CH_GROW, up to 2^15): many keys that weigh under 2^-25 of the
   // largest, float16's last step, may count for something together.
-  constexpr float UP = FMT ? 0.f : 7.f;
+  constexpr float UP = FMT ? 0.f : (BITS == 16 ? 7.f : 6.f);  // (over codes they are up to twice as large)
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   next_may_start();
@@ -524,7 +538,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   b.rfull = b.empty + C::NST;
   b.rempty = b.rfull + C::NRAW;
   b.scales = b.rempty + C::NRAW;
-  b.jfull = b.scales + C::NSC;
+  b.parts = b.scales + C::NSC;
+  b.jfull = b.parts + C::NSC;
   b.jempty = b.jfull + 2;
   b.qfull = b.jempty + 2;
   b.qfree = b.qfull + 2;
@@ -546,7 +561,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       mbar_init(&b.rfull[i], 1);
       mbar_init(&b.rempty[i], 4);
     }
-    for (int i = 0; i < C::NSC; ++i) mbar_init(&b.scales[i], 1);
+    for (int i = 0; i < C::NSC; ++i) {
+      mbar_init(&b.scales[i], 1);
+      mbar_init(&b.parts[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.jfull[i], 1);
       mbar_init(&b.jempty[i], 11 + C::CONV / 32);  // softmax, issuing, query and converting warps
@@ -632,12 +650,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         const float* scales = nullptr;
         if constexpr (BITS < 16) {
           // (the scores are there, so the scales of all earlier tiles have come)
-          const uint32_t at = before + j, turn = at / C::NSC;
-          if (!mbar_wait(&b.scales[at - turn * C::NSC], turn & 1u, CH_WAIT)) {
+          const uint32_t at = before + j, turn = at / C::NSC, place = at - turn * C::NSC;
+          if (!mbar_wait(&b.scales[place], turn & 1u, CH_WAIT) || !mbar_wait(&b.parts[place], turn & 1u, CH_WAIT)) {
             ok = false;
             break;
           }
-          scales = reinterpret_cast<const float*>(smem + C::SCALES) + (at - turn * C::NSC) * CH_KEYS;
+          scales = reinterpret_cast<const float*>(smem + C::SCALES) + place * 2 * CH_KEYS;
         }
         __syncwarp();  // tensor memory is read by whole warps, and a wait ends thread by thread
         tc_fence_after();
@@ -841,9 +859,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       const int box = min(1 << a.page_shift, BITS == 16 ? CH_KEYS : CH_RAW), boxes = CH_KEYS / box;
       int ji = 0;
       uint32_t jph = 1u;
-      // The scales of a tile's keys come with the first half of its values.  That waits for the values before to be
-      // converted, whose operands have the place of values NST / 2 tiles back: the softmax is past that tile, and so past
-      // the last user of the scales' place.
+      // The scales of a tile's keys and values come with the first half of its values, when the place of these values'
+      // operands is free: the softmax is past the tile that had it, and so past the last user of the scales' place.
       Ring<C::NSC ? C::NSC : 1> keyed;
       int scaled = 0;
       auto tell = [&](const Job& job) {
@@ -916,24 +933,29 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                   break;
                 }
                 if (kv == 1 && hf == 0) {
-                  if (lane == 0) mbar_arrive_expect_tx(&b.scales[keyed.i], static_cast<uint32_t>(n * box * 4));
+                  if (!mbar_wait(&b.empty[2 * keyed.i + 1], keyed.ph ^ 1u, CH_WAIT)) {
+                    ok = false;
+                    break;
+                  }
+                  if (lane == 0) mbar_arrive_expect_tx(&b.scales[keyed.i], static_cast<uint32_t>(n * box * 8));
                   __syncwarp();
-                  if (lane < n)
-                    bulk_load(smem + C::SCALES + (keyed.i * CH_KEYS + lane * box) * 4, a.ks + at, box * 4, &b.scales[keyed.i]);
+                  if (lane < n) {
+                    uint8_t* to = smem + C::SCALES + (keyed.i * 2 * CH_KEYS + lane * box) * 4;
+                    bulk_load(to, a.ks + at, box * 4, &b.scales[keyed.i]);
+                    bulk_load(to + CH_KEYS * 4, a.vs + at, box * 4, &b.scales[keyed.i]);
+                  }
                   ++scaled;
                   keyed.step();
                 }
-                uint8_t* dst = smem + C::raw_off(raw.i);
+                uint8_t* dst = smem + C::ROFF + raw.i * C::RAW;
                 const int b0 = hf * (boxes / 2), nb = max(0, min(boxes / 2, n - b0));
-                if (lane == 0)
-                  mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(nb * box * (C::ROW + (kv ? 5 : 1))));
+                if (lane == 0) mbar_arrive_expect_tx(&b.rfull[raw.i], static_cast<uint32_t>(nb * box * (C::ROW + 1)));
                 __syncwarp();
                 if (lane >= b0 && lane < b0 + nb) {
                   const int x = (lane - b0) * box;
                   const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.vc : a.kc) + at * C::ROW;
                   bulk_load(dst + x * C::ROW, codes, box * C::ROW, &b.rfull[raw.i]);
                   bulk_load(dst + CH_RAW * C::ROW + x, (kv ? a.vz : a.kz) + at, box, &b.rfull[raw.i]);
-                  if (kv) bulk_load(dst + CH_RAW * (C::ROW + 1) + x * 4, a.vs + at, box * 4, &b.rfull[raw.i]);
                 }
                 ++issued;
                 raw.step();
@@ -1037,56 +1059,79 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             break;
           }
           uint8_t* tile = smem + C::RING + at * C::TILE;
-          constexpr int STEP = 128 / PPR, N = CH_RAW / STEP;  // rows between pieces, pieces of a thread
-          constexpr int WORDS = BITS / 2;                     // of a piece
+          if (kv && !mbar_wait(&b.scales[at >> 1], ph, CH_WAIT)) {
+            ok = false;
+            break;
+          }
+          float* scales = reinterpret_cast<float*>(smem + C::SCALES) + ((at >> 1) * 2 + 1) * CH_KEYS;  // of the values
+          // A thread's pieces: NA of each half, STEP rows apart, N at a time (all at once, their instructions twice in the
+          // cache: 720 us for the long chunk of 8 bits, 709 so).
+          constexpr int STEP = 128 / PPR, NA = CH_RAW / STEP, N = NA / 2;
+          constexpr int WORDS = BITS / 2;  // of a piece
           for (int hf = 0; hf < 2; ++hf) {
             const int rs = 2 * kv + hf;
             if (!mbar_wait(&b.rfull[rs], rph, CH_WAIT)) {
               ok = false;
               break;
             }
-            const uint8_t* src = smem + C::raw_off(rs);
+            const uint8_t* src = smem + C::ROFF + rs * C::RAW;
             uint8_t* dst = tile + hf * CH_RAW * 128;
             const int left = rest - hf * CH_RAW;
-            uint32_t wd[N][WORDS];
-            float sc[N], zf[N];
+#pragma unroll 1
+            for (int r1 = r0; r1 < CH_RAW; r1 += N * STEP) {
+              uint32_t wd[N][WORDS];
+              float sc[N], zf[N];
 #pragma unroll
-            for (int x = 0; x < N; ++x) {
-              const int r = r0 + x * STEP;
-              if constexpr (BITS == 8)
-                *reinterpret_cast<uint4*>(wd[x]) = *reinterpret_cast<const uint4*>(src + r * C::ROW + col * 16);
-              else
-                *reinterpret_cast<uint2*>(wd[x]) = *reinterpret_cast<const uint2*>(src + r * C::ROW + col * 8);
-              // values past the last: zeros (keys there: scores that no row sees)
-              sc[x] = KEY_STEP;
-              if (kv) sc[x] = r < left ? *reinterpret_cast<const float*>(src + CH_RAW * (C::ROW + 1) + r * 4) : 0.f;
-              zf[x] = __uint_as_float(0x4B000000u | src[CH_RAW * C::ROW + r]);  // 2^23 + zero
-            }
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-              const float2 s2 = make_float2(sc[x], sc[x]), z2 = make_float2(-zf[x], -zf[x]);
-              uint32_t out[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float2 f;
-                if constexpr (BITS == 8) {
-                  const uint32_t v = wd[x][e >> 1];
-                  f.x = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650u + (e & 1) * 2));
-                  f.y = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651u + (e & 1) * 2));
-                } else {
-                  const uint32_t v = wd[x][e >> 2] >> ((e & 3) * 8);
-                  f.x = __uint_as_float((v & 15u) | 0x4B000000u);
-                  f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
-                }
-                f = mul2(add2(f, z2), s2);  // the difference is exact
-                out[e] = pack2<T>(f.x, f.y);
+              for (int x = 0; x < N; ++x) {
+                const int r = r1 + x * STEP;
+                if constexpr (BITS == 8)
+                  *reinterpret_cast<uint4*>(wd[x]) = *reinterpret_cast<const uint4*>(src + r * C::ROW + col * 16);
+                else
+                  *reinterpret_cast<uint2*>(wd[x]) = *reinterpret_cast<const uint2*>(src + r * C::ROW + col * 8);
+                // values past the last: zeros (keys there: scores that no row sees)
+                sc[x] = KEY_STEP;
+                if (kv) sc[x] = r < left ? power_of(scales[hf * CH_RAW + r]) : 0.f;
+                zf[x] = __uint_as_float(0x4B000000u | src[CH_RAW * C::ROW + r]);  // 2^23 + zero
               }
-              // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
-              const int r = r0 + x * STEP;
-              const bool o = (col & 4) != 0;
-              const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
-              *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 1 : 0))) = o ? hi : lo;
-              *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 0 : 1))) = o ? lo : hi;
+#pragma unroll
+              for (int x = 0; x < N; ++x) {
+                const float2 s2 = make_float2(sc[x], sc[x]), z2 = make_float2(-zf[x], -zf[x]);
+                uint32_t out[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  float2 f;
+                  if constexpr (BITS == 8) {
+                    const uint32_t v = wd[x][e >> 1];
+                    f.x = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650u + (e & 1) * 2));
+                    f.y = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651u + (e & 1) * 2));
+                  } else {
+                    const uint32_t v = wd[x][e >> 2] >> ((e & 3) * 8);
+                    f.x = __uint_as_float((v & 15u) | 0x4B000000u);
+                    f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
+                  }
+                  f = mul2(add2(f, z2), s2);  // exact
+                  if constexpr (FMT)  // bfloat16 holds it in the upper half
+                    out[e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632u);
+                  else
+                    out[e] = pack2<T>(f.x, f.y);
+                }
+                // the columns of the second 64 elements store their odd chunk first: no two of 8 neighbours on a bank
+                const int r = r1 + x * STEP;
+                const bool o = (col & 4) != 0;
+                const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
+                *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 1 : 0))) = o ? hi : lo;
+                *reinterpret_cast<uint4*>(dst + chunk_off(r, 2 * col + (o ? 0 : 1))) = o ? lo : hi;
+              }
+            }
+            if (kv) {  // the parts of the scales, for the softmax: a row per lane, of those that the warp has converted
+              constexpr int NB = 32 / PPR;
+              __syncwarp();
+              if (lane < NB * NA) {
+                float* scale = scales + hf * CH_RAW + (tid >> 5) * NB + lane % NB + lane / NB * STEP;
+                *scale = part_of(*scale);
+              }
+              __syncwarp();
+              if (hf == 1 && lane == 0) mbar_arrive(&b.parts[at >> 1]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.rempty[rs]);
