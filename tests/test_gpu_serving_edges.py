@@ -296,3 +296,31 @@ def test_values_behind_codes_of_any_size(bits, n, size):
     v *= torch.logspace(-8, 8, L, base=10.0)[torch.randperm(L)][:, None, None] if size == "mixed" else size
     c = _case([L], [n], H, D, 16, bits, dtype, 5, kv=lambda s, L: (_randn((L, H, D), 5, dtype), v.to(dtype)), Hq=H * group)
     _check(c, _attend(c, bits), [n], dtype, bits)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 40, 200])
+def test_float16_calls_over_values_past_their_range(bits, D, n):
+    """Values behind codes of 1e5, 2^40 in one channel of one key: the answer is in float16's range where they weigh
+    little, and infinite where not."""
+    H, group, L, dtype = 1, 4, max(n, 220), torch.bfloat16
+
+    def kv(s, L):
+        k, v = _randn((L, H, D), 5, dtype), _randn((L, H, D), 6, dtype)
+        v[7] *= 1e5
+        k[7] = 0.0
+        v[11, :, 3] = 2.0 ** 40
+        return k, v
+
+    c = _case([L], [n], H, D, 32, bits, dtype, 5, kv=kv, Hq=H * group)
+    c["q"] = c["q"].half()
+    out, (k, v) = _attend(c, bits), c["vals"][0]
+    q = _np(c["q"][:n])
+    ref, mass, size = R.attention(q, k, v)
+    most = _bound(c, 0, q, n * group, ref, mass, size, torch.float16, bits)
+    out = _np(out)
+    over = np.abs(ref) - most > 65520
+    assert over.any() and np.all(np.isinf(out[over]) & (np.sign(out[over]) == np.sign(ref[over])))
+    fine = np.abs(ref) + most < 65504
+    assert fine.any() and np.all(np.abs(out - ref)[fine] <= most[fine])
