@@ -18,8 +18,8 @@
 //    power of two, exact too, and the rest of the scale multiplies the probabilities in fp32, before they are rounded.
 //    So nothing behind a code is rounded, nor a query, whatever its size; what remains is the rounding of the weights,
 //    as over a 16-bit cache.  (All multiplied out and rounded, keys and bfloat16 queries to float16, values to q's type,
-//    a long cache of 8 bits took 13 % less time: scores were -infinity, unnoticed, where 65504 was exceeded, and errors
-//    1.7 times those of an answer in fp32 rounded once, now 1.36.)  A float16 call's value past that type's range is
+//    a long cache of 8 bits took 11 % less time: scores were -infinity, unnoticed, where 65504 was exceeded, and errors
+//    1.7 times those of an answer in fp32 rounded once, now 1.41.)  A float16 call's value past that type's range is
 //    infinite, makes its rows infinite or NaN, and is found by the second look.
 //  * The running maximum moves only when it grows by more than 8 (base 2): until then probabilities
 //    reach 2^8 at most, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         float x[KEEP][32];
         float top = -INFINITY;
         // (Two turns of one loop over codes: unrolled as well, the converters and the softmax miss the instruction
-        // cache more, 691 us instead of 673 for the long chunk of 8 bits, 346 instead of 319 for prompts.)
+        // cache more, by 3 % over a long chunk of 8 bits and 8 % in prompts.)
 #pragma unroll 1
         for (int c = 4 - KEEP; c >= 0; c -= KEEP) {
 #pragma unroll
@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
           float* scales = reinterpret_cast<float*>(smem + C::SCALES) + ((at >> 1) * 2 + 1) * CH_KEYS;  // of the values
           // A thread's pieces: NA of each half, STEP rows apart, N at a time (all at once, their instructions twice in the
-          // cache: 720 us for the long chunk of 8 bits, 709 so).
+          // cache: prompts of 2048 over 8 bits 357 us, 346 so).
           constexpr int STEP = 128 / PPR, NA = CH_RAW / STEP, N = NA / 2;
           constexpr int WORDS = BITS / 2;  // of a piece
           for (int hf = 0; hf < 2; ++hf) {
@@ -1095,7 +1095,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               }
 #pragma unroll
               for (int x = 0; x < N; ++x) {
-                const float2 s2 = make_float2(sc[x], sc[x]), z2 = make_float2(-zf[x], -zf[x]);
+                // (2^23 + code) s - (2^23 + zero) s: no step of it rounds, s being a power of two
+                const float2 s2 = make_float2(sc[x], sc[x]), z2 = make_float2(-zf[x] * sc[x], -zf[x] * sc[x]);
                 uint32_t out[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -1109,7 +1110,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                     f.x = __uint_as_float((v & 15u) | 0x4B000000u);
                     f.y = __uint_as_float(((v >> 4) & 15u) | 0x4B000000u);
                   }
-                  f = mul2(add2(f, z2), s2);  // exact
+                  f = fma2(f, s2, z2);
                   if constexpr (FMT)  // bfloat16 holds it in the upper half
                     out[e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632u);
                   else
