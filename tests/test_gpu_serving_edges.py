@@ -324,3 +324,25 @@ def test_float16_calls_over_values_past_their_range(bits, D, n):
     assert over.any() and np.all(np.isinf(out[over]) & (np.sign(out[over]) == np.sign(ref[over])))
     fine = np.abs(ref) + most < 65504
     assert fine.any() and np.all(np.abs(out - ref)[fine] <= most[fine])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("have,n", [(260, 200), (40, 4), (3000, 2)])
+def test_unseen_minus_infinity(dtype, bits, have, n):
+    """As test_attention_unseen_nonfinite, with -infinity: it reaches the rows that see it and no others."""
+    D, H, bad = 64, 2, have - n // 2
+
+    def kv(s, L):
+        k, v = _randn((L, H, D), 1, dtype), _randn((L, H, D), 2, dtype)
+        k[bad, 0, 3] = v[bad] = -float("inf")
+        return k, v
+
+    c = _case([have], [n], H, D, 16, bits, dtype, 3, kv=kv, Hq=4)
+    out, first = _np(_attend(c, bits)), bad - (have - n)
+    k, v = c["vals"][0]
+    c["vals"][0] = k[:bad], v[:bad]
+    q = _np(c["q"][:first])
+    ref, mass, size = R.attention(q, k[:bad], v[:bad])
+    assert np.all(np.abs(out[:first] - ref) <= _bound(c, 0, q, n * 2, ref, mass, size, dtype, bits))
+    assert not np.isfinite(out[first:]).any()
