@@ -21,17 +21,18 @@
 //    a long cache of 8 bits took 11 % less time: scores were -infinity, unnoticed, where 65504 was exceeded, and errors
 //    1.7 times those of an answer in fp32 rounded once, now 1.41.)  A float16 call's value past that type's range is
 //    infinite, makes its rows infinite or NaN, and is found by the second look.
-//  * The running maximum moves only when it grows by more than 8 (base 2): until then probabilities
-//    reach 2^8 at most, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
+//  * The running maximum moves only when it grows by more than 8 (base 2): until then weights reach 2^8 times what
+//    they are held against, harmless in fp32 sums and 16-bit operands, and the accumulator needs no rescaling.
 //  * The (row tile, 128 keys) units of the batch are cut into equal shares, one per SM, as in the
 //    kernel for few rows; cut tiles are joined by a second launch in a fixed order.
 // Bound by the exponentials and the tensor core together: 128 x 128 scores take 512 cycles of the
 // tensor core twice and 1024 cycles of the 16-per-cycle exponential unit.  A half's turn takes about 2000 cycles
 // of softmax and 850 of waiting for its products, and two halves share the tensor core: 1.15-1.24 PFLOP/s over a
-// long 16-bit cache (1024 new tokens, 64 heads over 8, 16384 keys: 436-450 us; the clock falls to 1.4 GHz).
-// Codes cost the converters' instructions and shared-memory traffic beside the tensor core's own: 616 us in 8
-// bits, 710 in 4.  Short prompts pay for each tile's start and end, about 9500 of 37000 cycles (four of 2048, 32
-// heads: 188 us).
+// long 16-bit cache (1024 new tokens, 64 heads over 8, 16384 keys: 436 us; the clock falls to 1.4 GHz).
+// Codes cost the converters' instructions, the scales' in the softmax and shared-memory traffic beside the tensor
+// core's own: 721 us in 8 bits among calls with other inputs (691 from a graph that replays one), 742 (736) in 4.  Short
+// prompts pay for each tile's start and end, about 9500 of 37000 cycles (four of 2048, 32 heads: 219 us, 187 from a
+// graph).
 #include <cuda.h>
 
 #include <algorithm>

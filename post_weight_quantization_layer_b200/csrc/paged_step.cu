@@ -6,7 +6,8 @@
 //  * The rows of all query heads that share a kv head (row i * group + g) are the 8 (or 2 x 8) columns of the
 //    16x8x16 matrix instruction, keys, and then the columns of the values, its 16 rows: a cache line is read
 //    once, and up to 8 rows cost half the products and accumulators of a 16-row tile (64 users of 70B-shaped
-//    heads, 8 bits: 148 -> 118 us; four users, 131072 keys, 4 bits: 249 -> 183 us).
+//    heads, 8 bits: 148 -> 118 us; four users, 131072 keys, 4 bits: 249 -> 183 us; as it stands 115 and 186 from a
+//    graph that replays one input, 132 and 190 among calls with others).
 //  * Each warp has its own ring of steps in shared memory, filled by asynchronous copies one to seven steps
 //    ahead (17 KB a warp, 200 KB an SM): the bytes in flight that the memory's latency asks for do not fit in
 //    registers (prefetching there: 32 KB an SM, 8-bit cache at 3.4 TB/s; now 5.4).
@@ -20,7 +21,7 @@
 //    a long context is small, and an offset taken off after it left 0.39 of it wrong at 131072 keys of 4 bits.
 //    Keys keep their offset, which a contraction over one head affords: q . (c - z) = q . (o + c) - (o + z) sum(q).
 //    A key's scale multiplies its scores, a value's scale its probability: no value is rounded.  The query is
-//    brought into float16's range by a power of two per row, and the weights w_j = p_j scale_j are held against
+//    brought to the upper end of float16's range by a power of two per row, and the weights w_j = p_j scale_j are held against
 //    their own running maximum, so that float16 (2^-11) holds them whatever the scales are.  (Converting
 //    pair by pair to 16 bits through fp32: 44 instructions per key and head of 128.)
 //  * The keys of all sequences are one line of 64-key units, cut into equal shares, one per resident
@@ -28,7 +29,8 @@
 //    unfinished (sequence, head) pieces, its first and its last; those leave (maximum, sum, weighted
 //    sum) behind and a second launch joins them in order, so results do not depend on timing.
 //  * Few items of short contexts go to clusters of CTAs instead, an item each, which join through shared
-//    memory in the same launch (one user, 32 heads, 2500 keys: 16.2 -> 11.7 us; its bytes take 6.4).
+//    memory in the same launch (one user, 32 heads, 2500 keys: 16.2 -> 11.7 us, 12.7 among calls with other inputs; its
+//    bytes take 6.4).
 // Each warp walks its own keys with its own running maximum and sum (fp32).
 #include <algorithm>
 #include <type_traits>

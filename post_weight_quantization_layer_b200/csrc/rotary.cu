@@ -10,7 +10,8 @@
 // compute the tokens' cosines and sines once into shared memory (64 double products per token
 // of 128-wide heads, shared by all heads), then walk the (token, head, 8 pairs) items, 32
 // bytes each, neighbouring threads on neighbouring chunks of a head.  16384 tokens of 64 + 8
-// heads of 128: 99 us, 6.1 TB/s; 8 tokens of 32 + 32: 2.8 us, a launch.
+// heads of 128: 108 us and 5.6 TB/s among calls with other inputs (99 and 6.1 from a graph that replays one); 8 tokens
+// of 32 + 32: 2.4 us, a launch.  Where rotary_dim is no multiple of 16, value by value: 781 us with 20 of 128 rotated.
 #include <math.h>
 
 #include <algorithm>
