@@ -463,7 +463,8 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 }
 
 struct Bars {
-  uint64_t *full, *empty, *rfull, *rempty, *scales, *parts, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull, *odone, *zero, *done;
+  uint64_t *full, *empty, *rfull, *rempty, *scales, *parts, *jfull, *jempty, *qfull, *qfree, *sfull, *pmost, *pfull;
+  uint64_t *odone, *zero, *done;
 };
 
 // What the other warps have to know of a piece, as the warp that walks the line tells them through shared

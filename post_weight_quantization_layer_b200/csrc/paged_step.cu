@@ -21,9 +21,9 @@
 //    a long context is small, and an offset taken off after it left 0.39 of it wrong at 131072 keys of 4 bits.
 //    Keys keep their offset, which a contraction over one head affords: q . (c - z) = q . (o + c) - (o + z) sum(q).
 //    A key's scale multiplies its scores, a value's scale its probability: no value is rounded.  The query is
-//    brought to the upper end of float16's range by a power of two per row, and the weights w_j = p_j scale_j are held against
-//    their own running maximum, so that float16 (2^-11) holds them whatever the scales are.  (Converting
-//    pair by pair to 16 bits through fp32: 44 instructions per key and head of 128.)
+//    brought to the upper end of float16's range by a power of two per row, and the weights w_j = p_j scale_j are
+//    held against their own running maximum, so that float16 (2^-11) holds them whatever the scales are.
+//    (Converting pair by pair to 16 bits through fp32: 44 instructions per key and head of 128.)
 //  * The keys of all sequences are one line of 64-key units, cut into equal shares, one per resident
 //    CTA: ragged lengths balance, and one long sequence fills the GPU.  A CTA's share has at most two
 //    unfinished (sequence, head) pieces, its first and its last; those leave (maximum, sum, weighted
